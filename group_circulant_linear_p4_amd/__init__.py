@@ -6,7 +6,10 @@ cyclic shifts, W[d*T+g, c*T+h] = w[d, c, (g-h) mod T] ("Insight Central" in
 per-frequency channel GEMMs on the half spectrum and the inverse DFT, all in
 hand-written HIP kernels for gfx950 behind the C ABI in include/eqlinear.h.
 
-This module is the thin ctypes binding of that ABI: one Python function per C
+include/eqlinear_block.h adds the operators around the layer in a transformer block: the
+equivariant layer norm and 8-bit activation checkpoints with the passes that read them.
+
+This module is the thin ctypes binding of both headers: one Python function per C
 entry point, with the same name and argument order.  Buffers may be given as
 torch tensors on a ROCm device or as raw device addresses (int); `stream` as a
 torch.cuda.Stream, a raw hipStream_t (int) or None for torch's current stream.
@@ -28,6 +31,10 @@ __all__ = [
     "eqlinear_bwd_w_workspace_bytes", "eqlinear_bwd_w",
     "eqlinear_fwd_train", "eqlinear_fwd_fused_train", "eqlinear_bwd_x_train", "eqlinear_bwd_w_train",
     "eqlinear_p4m_expand_weight", "eqlinear_p4m_fold_weight_grad",
+    "eqlinear_block_abi_version", "eqlinear_ckpt8_bytes", "eqlinear_ckpt8_pack", "eqlinear_ckpt8_unpack",
+    "eqlinear_layernorm_fwd", "eqlinear_layernorm_bwd_workspace_bytes", "eqlinear_layernorm_bwd",
+    "eqlinear_layernorm_bwd_ckpt8", "eqlinear_fused_epilogue_bwd_ckpt8", "eqlinear_bwd_w_ckpt8",
+    "eqlinear_ckpt8_spectrum",
 ]
 
 EQL_F32, EQL_F16 = 0, 1
@@ -97,6 +104,20 @@ def lib() -> ctypes.CDLL:
         L.eqlinear_fwd_fused_train.restype = i32
         L.eqlinear_bwd_w_train.argtypes = [vp, vp, vp, sz, i64, i64, i64, i32, i32, vp]
         L.eqlinear_bwd_w_train.restype = i32
+        f32 = ctypes.c_float
+        for name, args, res in (
+                ("eqlinear_block_abi_version", [], i32),
+                ("eqlinear_ckpt8_bytes", [i64, i64, i32], sz),
+                ("eqlinear_ckpt8_pack", [vp, vp, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_ckpt8_unpack", [vp, vp, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_layernorm_fwd", [vp] * 7 + [i64, i64, i32, f32, i32, vp], i32),
+                ("eqlinear_layernorm_bwd_workspace_bytes", [i64, i64, i32, i32], sz),
+                ("eqlinear_layernorm_bwd", [vp] * 10 + [sz, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_layernorm_bwd_ckpt8", [vp] * 9 + [sz, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_fused_epilogue_bwd_ckpt8", [vp] * 5 + [sz, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_bwd_w_ckpt8", [vp, vp, vp, i32, vp, vp, vp, sz, i64, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_ckpt8_spectrum", [vp, vp, vp, i32, vp, sz, i64, i64, i64, i32, i32, vp], i32)):
+            getattr(L, name).argtypes, getattr(L, name).restype = args, res
         _lib = L
     return _lib
 
@@ -251,3 +272,75 @@ def eqlinear_p4m_fold_weight_grad(dw_c4, dw, Dp: int, Cp: int, dtype, stream=Non
     """C_4 weight gradient [2Dp][2Cp][4] -> the p4m weight gradient [Dp][Cp][8]."""
     _check(lib().eqlinear_p4m_fold_weight_grad(_ptr(dw_c4), _ptr(dw), Dp, Cp, _dtype(dtype), _stream(stream)),
            "eqlinear_p4m_fold_weight_grad")
+
+
+# include/eqlinear_block.h: layer norm and 8-bit activation checkpoints.
+def eqlinear_block_abi_version() -> int:
+    return lib().eqlinear_block_abi_version()
+
+
+def eqlinear_ckpt8_bytes(N: int, Cp: int, T: int) -> int:
+    return lib().eqlinear_ckpt8_bytes(N, Cp, T)
+
+
+def eqlinear_ckpt8_pack(x, ckpt, N: int, Cp: int, T: int, dtype, stream=None) -> None:
+    """x [N][Cp*T] -> its 8-bit checkpoint."""
+    _check(lib().eqlinear_ckpt8_pack(_ptr(x), _ptr(ckpt), N, Cp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_ckpt8_pack")
+
+
+def eqlinear_ckpt8_unpack(ckpt, x, N: int, Cp: int, T: int, dtype, stream=None) -> None:
+    """The checkpoint's values -> x [N][Cp*T]."""
+    _check(lib().eqlinear_ckpt8_unpack(_ptr(ckpt), _ptr(x), N, Cp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_ckpt8_unpack")
+
+
+def eqlinear_layernorm_fwd(x, gamma, beta, y, ckpt, mean, rstd, N: int, Cp: int, T: int, eps: float, dtype,
+                           stream=None) -> None:
+    """gamma / beta / ckpt / mean / rstd may be None; y may be x."""
+    _check(lib().eqlinear_layernorm_fwd(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(ckpt), _ptr(mean), _ptr(rstd),
+                                        N, Cp, T, float(eps), _dtype(dtype), _stream(stream)),
+           "eqlinear_layernorm_fwd")
+
+
+def eqlinear_layernorm_bwd_workspace_bytes(N: int, Cp: int, T: int, dtype) -> int:
+    return lib().eqlinear_layernorm_bwd_workspace_bytes(N, Cp, T, _dtype(dtype))
+
+
+def eqlinear_layernorm_bwd(dy, x, mean, rstd, gamma, dres, dx, dgamma, dbeta, workspace, ws_bytes: int, N: int,
+                           Cp: int, T: int, dtype, stream=None) -> None:
+    """gamma / dres / dgamma / dbeta may be None; dx may be dy or dres."""
+    _check(lib().eqlinear_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(gamma), _ptr(dres), _ptr(dx),
+                                        _ptr(dgamma), _ptr(dbeta), _ptr(workspace), int(ws_bytes), N, Cp, T,
+                                        _dtype(dtype), _stream(stream)), "eqlinear_layernorm_bwd")
+
+
+def eqlinear_layernorm_bwd_ckpt8(dy, ckpt, rstd, gamma, dres, dx, dgamma, dbeta, workspace, ws_bytes: int, N: int,
+                                 Cp: int, T: int, dtype, stream=None) -> None:
+    """eqlinear_layernorm_bwd with the normalised rows read from the forward's checkpoint."""
+    _check(lib().eqlinear_layernorm_bwd_ckpt8(_ptr(dy), _ptr(ckpt), _ptr(rstd), _ptr(gamma), _ptr(dres), _ptr(dx),
+                                              _ptr(dgamma), _ptr(dbeta), _ptr(workspace), int(ws_bytes), N, Cp, T,
+                                              _dtype(dtype), _stream(stream)), "eqlinear_layernorm_bwd_ckpt8")
+
+
+def eqlinear_fused_epilogue_bwd_ckpt8(dy, pre_ckpt, dpre, dbias, workspace, ws_bytes: int, N: int, Dp: int, T: int,
+                                      dtype, stream=None) -> None:
+    """The GELU epilogue's backward with GELU's input read from a checkpoint; dbias may be None."""
+    _check(lib().eqlinear_fused_epilogue_bwd_ckpt8(_ptr(dy), _ptr(pre_ckpt), _ptr(dpre), _ptr(dbias), _ptr(workspace),
+                                                   int(ws_bytes), N, Dp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_fused_epilogue_bwd_ckpt8")
+
+
+def eqlinear_bwd_w_ckpt8(ckpt, gamma, beta, act: int, dy, dw, workspace, ws_bytes: int, N: int, Cp: int, Dp: int,
+                         T: int, dtype, stream=None) -> None:
+    """eqlinear_bwd_w with the layer's input act(gamma value + beta) read from a checkpoint."""
+    _check(lib().eqlinear_bwd_w_ckpt8(_ptr(ckpt), _ptr(gamma), _ptr(beta), int(act), _ptr(dy), _ptr(dw),
+                                      _ptr(workspace), int(ws_bytes), N, Cp, Dp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_bwd_w_ckpt8")
+
+
+def eqlinear_ckpt8_spectrum(ckpt, gamma, beta, act: int, workspace, ws_bytes: int, N: int, Cp: int, Dp: int, T: int,
+                            dtype, stream=None) -> None:
+    """That input's half spectrum into the weight-gradient workspace, as eqlinear_fwd_train leaves it."""
+    _check(lib().eqlinear_ckpt8_spectrum(_ptr(ckpt), _ptr(gamma), _ptr(beta), int(act), _ptr(workspace), int(ws_bytes),
+                                         N, Cp, Dp, T, _dtype(dtype), _stream(stream)), "eqlinear_ckpt8_spectrum")

@@ -41,6 +41,11 @@ SOURCES = [
     "eql_bwdw4.hip",
     "eql_epi.hip",
     "eql_p4m.hip",
+    "eql_block_api.hip",
+    "eql_ckpt8.hip",
+    "eql_spec8.hip",
+    "eql_norm_fwd.hip",
+    "eql_norm_bwd.hip",
 ]
 
 CFLAGS = [

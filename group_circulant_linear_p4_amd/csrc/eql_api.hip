@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "eql_block.h"
 #include "eql_launch.h"
 #include "eqlinear.h"
 
@@ -508,15 +509,49 @@ int epilogue_bwd(const void* dy, const void* pre, void* dpre, void* dbias, void*
   return EQL_OK;
 }
 
+// The checks of a checkpoint view's pointers (their alignment among them).
+int check_view(const host::CkptView& v, int64_t N, int dtype) {
+  if (v.act != EQL_ACT_NONE && v.act != EQL_ACT_GELU) return EQL_EINVAL;
+  if (N > 0 && !v.ckpt) return EQL_EINVAL;
+  const uintptr_t elt = (uintptr_t)elt_bytes(dtype);
+  if ((v.ckpt && !aligned16(v.ckpt)) || (v.gamma && reinterpret_cast<uintptr_t>(v.gamma) % elt != 0) ||
+      (v.beta && reinterpret_cast<uintptr_t>(v.beta) % elt != 0))
+    return EQL_EALIGN;
+  return EQL_OK;
+}
+
+// The half spectrum of a checkpointed N x K matrix into operand units, as run_spec's.
+int run_spec8(const host::CkptView& v, void* out, int64_t N, int64_t K, int64_t Kpad, int64_t kgCount, int T, int dtype,
+              hipStream_t s) {
+  const int64_t grid = ceil_div(kgCount * 2 * Kpad, 256);
+  if (grid > kMaxGrid) return EQL_EINVAL;
+  Spec8Args a{};
+  a.pitch = (int)ckpt_pitch(K * T);
+  a.codes = static_cast<const unsigned char*>(v.ckpt);
+  a.scales = a.codes + N * a.pitch;
+  a.gamma = v.gamma;
+  a.beta = v.beta;
+  a.act = v.act;
+  a.out = out;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.Kpad = (int)Kpad;
+  a.kgCount = (int)kgCount;
+  a.tw = make_twiddles(T);
+  return status_of(dtype == EQL_F16 ? launch_spec8_f16(T, a, (unsigned)grid, s) : launch_spec8_f32(T, a, (unsigned)grid, s));
+}
+
 // Body of the weight-gradient entry points.  spectra: the workspace already holds x's
 // spectrum and, on the separate path, dy's (written by the training forward and
-// input gradient); only the GEMMs and the reduce run, and x is not read.
+// input gradient); only the GEMMs and the reduce run, and x is not read.  view: x comes from
+// this checkpoint (x itself is not read).
 int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws_bytes, int64_t N, int64_t Cp,
-             int64_t Dp, int T, int dtype, void* stream, bool spectra) {
+             int64_t Dp, int T, int dtype, void* stream, bool spectra, const host::CkptView* view = nullptr) {
   int st = check_sizes(N, Cp, Dp, T, dtype);
   if (st != EQL_OK) return st;
+  if (view && (st = check_view(*view, N, dtype)) != EQL_OK) return st;
   const BwdwPlan p = plan_bwdw(N, Cp, Dp, T, dtype);
-  const bool needX = !spectra, needDy = !spectra || p.fused;
+  const bool needX = !spectra && !view, needDy = !spectra || p.fused;
   if (!dw || (N > 0 && ((needX && !x) || (needDy && !dy) || !workspace))) return EQL_EINVAL;
   if (ws_bytes < p.total()) return EQL_EINVAL;
   if (!aligned16(dw) || (N > 0 && ((needX && !aligned16(x)) || (needDy && !aligned16(dy)) || !aligned16(workspace))))
@@ -539,7 +574,8 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
   if (N > 0 && p.fused) {
     // x's spectrum only; dy is transformed inside the GEMM.
     if (!spectra) {
-      st = run_spec(x, ws, N, Cp, p.Cpad, p.kgCount, T, dtype, s);
+      st = view ? run_spec8(*view, ws, N, Cp, p.Cpad, p.kgCount, T, dtype, s)
+                : run_spec(x, ws, N, Cp, p.Cpad, p.kgCount, T, dtype, s);
       if (st != EQL_OK) return st;
     }
     Bwdw4Args a{};
@@ -560,7 +596,11 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
     if (launch_bwdw4(f16, T, p.fNB, a, (unsigned)fItems, s) != hipSuccess) return EQL_EHIP;
   } else if (N > 0) {
     hipError_t e = hipSuccess;
-    if (!spectra) {
+    if (view) {
+      st = run_spec8(*view, ws + p.dyhBytes, N, Cp, p.Cpad, p.kgCount, T, dtype, s);
+      if (st == EQL_OK) st = run_spec(dy, ws, N, Dp, p.Dpad, p.kgCount, T, dtype, s);
+      if (st != EQL_OK) return st;
+    } else if (!spectra) {
       // dy's and x's spectra in one launch: dy's workgroups first, then x's.
       SpecArgs sp{};
       sp.N = (int)N;
@@ -618,6 +658,37 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
 }
 
 }  // namespace
+
+namespace eql::host {
+
+int check_sizes(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) { return ::check_sizes(N, Cp, Dp, T, dtype); }
+
+void epilogue_rows(int64_t N, int64_t Dp, int T, int dtype, int64_t* rowsPerBlock, int64_t* rowBlocks, size_t* partBytes) {
+  const EpiPlan p = plan_epi(N, Dp, T, dtype);
+  *rowsPerBlock = p.rowsPerBlock;
+  *rowBlocks = p.rowBlocks;
+  *partBytes = p.partBytes;
+}
+
+int bwd_w_from_ckpt(const CkptView& view, const void* dy, void* dw, void* workspace, size_t ws_bytes, int64_t N,
+                    int64_t Cp, int64_t Dp, int T, int dtype, void* stream) {
+  return run_bwdw(nullptr, dy, dw, workspace, ws_bytes, N, Cp, Dp, T, dtype, stream, false, &view);
+}
+
+int spectrum_from_ckpt(const CkptView& view, void* workspace, size_t ws_bytes, int64_t N, int64_t Cp, int64_t Dp, int T,
+                       int dtype, void* stream) {
+  int st = ::check_sizes(N, Cp, Dp, T, dtype);
+  if (st != EQL_OK) return st;
+  if ((st = check_view(view, N, dtype)) != EQL_OK) return st;
+  if (N == 0) return EQL_OK;
+  const BwdwPlan p = plan_bwdw(N, Cp, Dp, T, dtype);
+  if (!workspace || ws_bytes < p.total()) return EQL_EINVAL;
+  if (!aligned16(workspace)) return EQL_EALIGN;
+  return run_spec8(view, static_cast<char*>(workspace) + p.dyhBytes, N, Cp, p.Cpad, p.kgCount, T, dtype,
+                   static_cast<hipStream_t>(stream));
+}
+
+}  // namespace eql::host
 
 extern "C" {
 

@@ -1,0 +1,313 @@
+// 8-bit activation checkpoints and the passes that read them.
+//
+// A training step keeps activations from the forward to the backward pass.  A checkpoint
+// holds an [N][R] matrix (R = C'*T features a row) in about a quarter of fp32's bytes: blocks
+// of 32 consecutive features of a row (the last one may be short) share one power-of-two step,
+//     a = max |v| over the block,  e = the smallest integer >= -126 with a 2^-e < 127.5,
+//     code = v 2^-e rounded to nearest even, in [-127, 127],   value = code 2^e,
+// so the error is at most half a step, 2^(e-1) <= a / 127.  A power-of-two step makes both
+// directions exact but for that one rounding: codes are the same whatever computed them, and a
+// code's value is exact in fp32 and, for values of ordinary size, in fp16.  A block that holds
+// an infinity or a NaN reads back as NaN throughout (a training step must not lose an
+// overflow).  Layout: N rows of P = 32 ceil(R / 32) signed bytes (codes past R are zero), then
+// N rows of P / 32 scale bytes e + 127 (255 marks the NaN block).
+//
+// Every kernel here streams its operands once.  A lane takes 8 consecutive features ("chunk":
+// 16 bytes of fp16, 32 of fp32, 8 of codes), so a block is four neighbouring lanes and its
+// maximum two cross-lane moves; rows of any length are read at the alignment of one element,
+// which the hardware's global loads allow, so an odd row costs no narrower loads.
+#pragma once
+
+#include "eql_device.h"
+#include "eql_fwd.h"
+
+namespace eql {
+
+constexpr int kCkptBlock = 32;
+// Bytes of one row of codes.
+__host__ __device__ constexpr int64_t ckpt_pitch(int64_t row) { return (row + kCkptBlock - 1) / kCkptBlock * kCkptBlock; }
+
+// Eight elements at element alignment.
+template <typename Elt>
+struct Chunk;
+template <>
+struct Chunk<_Float16> {
+  typedef _Float16 V __attribute__((ext_vector_type(8)));
+  typedef _Float16 VU __attribute__((ext_vector_type(8), aligned(2)));
+};
+template <>
+struct Chunk<float> {
+  typedef float V __attribute__((ext_vector_type(8)));
+  typedef float VU __attribute__((ext_vector_type(8), aligned(4)));
+};
+
+template <typename Elt>
+__device__ __forceinline__ typename Chunk<Elt>::V zero_chunk() {
+  return (typename Chunk<Elt>::V)(Elt)0;
+}
+
+// The chunk at p, of which `n` elements exist (the others are zero).  WHOLE: every chunk is
+// whole or missing (R a multiple of 8), so no element-wise tail is compiled.
+template <typename Elt, bool WHOLE>
+__device__ __forceinline__ typename Chunk<Elt>::V load_chunk8(const Elt* p, int n) {
+  typename Chunk<Elt>::V v = zero_chunk<Elt>();
+  if (n >= 8) {
+    v = *reinterpret_cast<const typename Chunk<Elt>::VU*>(p);
+  } else if (!WHOLE && n > 0) {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < n) v[e] = p[e];
+  }
+  return v;
+}
+
+template <typename Elt, bool WHOLE>
+__device__ __forceinline__ void store_chunk8(Elt* p, int n, const float (&f)[8]) {
+  if (n >= 8) {
+    typename Chunk<Elt>::VU v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (Elt)f[e];
+    *reinterpret_cast<typename Chunk<Elt>::VU*>(p) = v;
+  } else if (!WHOLE && n > 0) {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < n) p[e] = (Elt)f[e];
+  }
+}
+
+// Cross-lane moves inside a row of 16 lanes (DPP): neighbours 1 and 2 apart in a quad, the
+// mirror of 8 and of 16 lanes.
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppMirror8 = 0x141, kDppMirror16 = 0x140;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, dpp_move<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+
+// Scale byte of the block this lane's quad holds, from the lane's largest |v| (as bits: an
+// infinity or a NaN compares above every finite magnitude).  The exponent of 127.5 2^e is
+// e + 6 and its mantissa field 0x7F0000, so adding 0x10000 to the magnitude's bits carries
+// into the exponent exactly from 127.5 2^e on.
+__device__ __forceinline__ uint32_t block_scale(uint32_t top) {
+  top = max(top, dpp_move<kDppXor1>(top));
+  top = max(top, dpp_move<kDppXor2>(top));
+  const int s = (int)((top + 0x10000u) >> 23) - 6;
+  return top >= 0x7F800000u ? 255u : (uint32_t)max(s, 1);
+}
+
+// Codes of eight values under scale byte s, as two words.  v 2^-e + 1.5 2^23 in one fused
+// operation: the product is exact, the sum rounds to the integer (ties to even), and the
+// integer is in the low bits of the result.
+__device__ __forceinline__ u32x2 encode8(const float (&v)[8], uint32_t s) {
+  const float back = s == 255u ? 0.0f : __builtin_bit_cast(float, (254u - s) << 23);
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = __builtin_bit_cast(uint32_t, __builtin_fmaf(v[e], back, 12582912.0f));
+  u32x2 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(w[4 * h + 1], w[4 * h], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(w[4 * h + 3], w[4 * h + 2], 0x04000c0cu);
+    r[h] = lo | hi;
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu);
+  return top;
+}
+
+// The step 2^e of a scale byte (NaN for 255).
+__device__ __forceinline__ float scale_step(uint32_t s) {
+  return __builtin_bit_cast(float, s == 255u ? 0x7FC00000u : s << 23);
+}
+
+// Four codes of a word to values (exact: seven bits times a power of two).
+__device__ __forceinline__ void decode4(uint32_t w, float step, float* v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)(int)(int8_t)(w >> (8 * e)) * step;
+}
+__device__ __forceinline__ void decode8(u32x2 w, float step, float (&v)[8]) {
+  decode4(w[0], step, v);
+  decode4(w[1], step, v + 4);
+}
+
+struct CkptArgs {
+  const void* x;          // pack: read; unpack: written (as void*)
+  unsigned char* codes;   // [N][pitch]
+  unsigned char* scales;  // [N][pitch / 32]
+  int64_t chunks;         // N * pitch / 8
+  int R, rowChunks;       // rowChunks = pitch / 8
+};
+
+// Flat order over the chunks of all rows (pitch / 8 a row, a multiple of four, so a block's
+// four chunks are four neighbouring lanes).  A workgroup's first chunk is split into row and
+// offset once, in 64 bits; a lane adds its own offset and divides in 32 bits.
+template <typename Elt, bool WHOLE>
+__device__ __forceinline__ void chunk_place(const CkptArgs& a, int64_t first, int o, int64_t& row, int& f0, int& n) {
+  const int64_t row0 = first / a.rowChunks;
+  const uint32_t rest = (uint32_t)(first - row0 * a.rowChunks) + (uint32_t)o;
+  const uint32_t dr = rest / (uint32_t)a.rowChunks;
+  row = row0 + dr;
+  f0 = (int)(rest - dr * (uint32_t)a.rowChunks) * 8;
+  n = a.R - f0;
+}
+
+template <typename Elt, bool WHOLE>
+__global__ void __launch_bounds__(256) eql_ckpt_pack_kernel(const CkptArgs a) {
+  const int64_t first = (int64_t)blockIdx.x * 256;
+  const int64_t idx = first + threadIdx.x;
+  if (idx >= a.chunks) return;  // a multiple of four: a quad is live or not as a whole
+  int64_t row;
+  int f0, n;
+  chunk_place<Elt, WHOLE>(a, first, (int)threadIdx.x, row, f0, n);
+  const auto v = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+  const uint32_t s = block_scale(top_bits(f));
+  *reinterpret_cast<u32x2*>(a.codes + idx * 8) = encode8(f, s);
+  if ((threadIdx.x & 3) == 0) a.scales[idx >> 2] = (unsigned char)s;
+}
+
+template <typename Elt, bool WHOLE>
+__global__ void __launch_bounds__(256) eql_ckpt_unpack_kernel(const CkptArgs a) {
+  const int64_t first = (int64_t)blockIdx.x * 256;
+  const int64_t idx = first + threadIdx.x;
+  if (idx >= a.chunks) return;
+  int64_t row;
+  int f0, n;
+  chunk_place<Elt, WHOLE>(a, first, (int)threadIdx.x, row, f0, n);
+  const float step = scale_step(a.scales[idx >> 2]);
+  float f[8];
+  decode8(*reinterpret_cast<const u32x2*>(a.codes + idx * 8), step, f);
+  store_chunk8<Elt, WHOLE>(static_cast<Elt*>(const_cast<void*>(a.x)) + row * a.R + f0, n, f);
+}
+
+// Backward of the bias + GELU epilogue with GELU's input read from a checkpoint:
+//     dpre = dy GELU'(value),   part[row block][feature] = sum over the block's rows of dpre.
+// A workgroup takes `lanes` chunks across and 256 / lanes rows at a time down its block of
+// rows; the column sums of its row groups are added in a fixed order through LDS.
+struct Epi8Args {
+  const void* dy;
+  const unsigned char* codes;
+  const unsigned char* scales;
+  void* dpre;  // may be dy
+  float* part; // [rowBlocks][R] or null
+  int64_t N;
+  int R, pitch, lanes, groups, colBlocks, rowsPerBlock;
+};
+
+template <typename Elt, bool WHOLE>
+__global__ void __launch_bounds__(256) eql_epi8_kernel(const Epi8Args a) {
+  __shared__ float red[256][9];
+  const int grp = (int)threadIdx.x / a.lanes, l = (int)threadIdx.x - grp * a.lanes;
+  const int cb = (int)blockIdx.x % a.colBlocks, rb = (int)blockIdx.x / a.colBlocks;
+  const int f0 = (cb * a.lanes + l) * 8;
+  const int n = a.R - f0;
+  const int64_t r0 = (int64_t)rb * a.rowsPerBlock;
+  const int64_t r1 = min(a.N, r0 + a.rowsPerBlock);
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.0f;
+  if (grp < a.groups && n > 0) {
+    const Elt* dy = static_cast<const Elt*>(a.dy) + f0;
+    Elt* dpre = static_cast<Elt*>(a.dpre) + f0;
+    for (int64_t r = r0 + grp; r < r1; r += a.groups) {
+      const auto g = load_chunk8<Elt, WHOLE>(dy + r * a.R, n);
+      const u32x2 w = *reinterpret_cast<const u32x2*>(a.codes + r * a.pitch + f0);
+      const float step = scale_step(a.scales[r * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
+      float v[8], d[8];
+      decode8(w, step, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] = (float)g[e] * gelu_grad(v[e]);
+        s[e] += d[e];
+      }
+      store_chunk8<Elt, WHOLE>(dpre + r * a.R, n, d);
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = s[e];
+  __syncthreads();
+  if (grp == 0 && n > 0) {
+    for (int q = 1; q < a.groups; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += red[q * a.lanes + l][e];
+    store_chunk8<float, WHOLE>(a.part + (int64_t)rb * a.R + f0, n, s);
+  }
+}
+
+// x's half spectrum for the weight gradient, as eql_spec_kernel writes it, with the layer's
+// input rebuilt from a checkpoint: v = act(gamma[c] value + beta[c]).
+struct Spec8Args {
+  const unsigned char* codes;
+  const unsigned char* scales;
+  const void* gamma;  // [K] or null
+  const void* beta;   // [K] or null
+  void* out;          // units [kgCount][T][2][Kpad]
+  int N, K, Kpad, kgCount, pitch, act;
+  Twiddles tw;
+};
+
+template <int T, typename Elt>
+__global__ void __launch_bounds__(256) eql_spec8_kernel(const Spec8Args a) {
+  using E = EltT<Elt>;
+  constexpr int G = E::kPerUnit;
+  const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (idx >= (size_t)a.kgCount * 2 * a.Kpad) return;
+  const int k = (int)(idx % a.Kpad);
+  const size_t rest = idx / a.Kpad;
+  const int half = (int)(rest & 1);
+  const int kg = (int)(rest >> 1);
+  const int row0 = kg * 2 * G + half * G;
+  const bool live = k < a.K;
+  const float gam = live && a.gamma ? (float)static_cast<const Elt*>(a.gamma)[k] : 1.0f;
+  const float bet = live && a.beta ? (float)static_cast<const Elt*>(a.beta)[k] : 0.0f;
+  // A channel's T features lie in one block of 32 where T divides 32, else in at most two.
+  constexpr bool ONE = kCkptBlock % T == 0;
+  const int b0 = k * T / kCkptBlock, b1 = (k * T + T - 1) / kCkptBlock;
+  const int cut = b1 * kCkptBlock - k * T;  // features from `cut` on take the second block's step
+  float pl[T][G];
+#pragma unroll
+  for (int e = 0; e < G; ++e) {
+    float v[T], o[T];
+    const int row = row0 + e;
+    if (row < a.N && live) {
+      const unsigned char* c = a.codes + (size_t)row * a.pitch + (size_t)k * T;
+      const unsigned char* sc = a.scales + (size_t)row * (a.pitch / kCkptBlock);
+      const float s0 = scale_step(sc[b0]);
+      const float s1 = ONE ? s0 : scale_step(sc[b1]);
+      uint32_t w[(T + 3) / 4];
+#pragma unroll
+      for (int i = 0; i < (T + 3) / 4; ++i) w[i] = 0;
+      __builtin_memcpy(w, c, T);
+#pragma unroll
+      for (int h = 0; h < T; ++h) {
+        const float step = ONE ? s0 : (b1 > b0 && h >= cut ? s1 : s0);
+        const int code = (int)(int8_t)(w[h / 4] >> (8 * (h % 4)));
+        float q = (float)code * step;
+        q = __builtin_fmaf(q, gam, bet);
+        v[h] = a.act == 1 ? gelu_erf(q) : q;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < T; ++h) v[h] = 0.0f;
+    }
+    Dft<T>::run(v, o, a.tw);
+#pragma unroll
+    for (int p = 0; p < T; ++p) pl[p][e] = o[p];
+  }
+  u32x4* out = static_cast<u32x4*>(a.out) + ((size_t)kg * T * 2 + half) * a.Kpad + k;
+#pragma unroll
+  for (int p = 0; p < T; ++p) __builtin_nontemporal_store(E::pack(pl[p]), &out[(size_t)p * 2 * a.Kpad]);
+}
+
+}  // namespace eql

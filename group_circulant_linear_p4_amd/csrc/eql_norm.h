@@ -1,0 +1,454 @@
+// Layer norm of an equivariant block, forward and backward.
+//
+// A row holds R = C'*T features.  Mean and variance are taken over the whole row, so a cyclic
+// shift of every channel's group axis leaves them alone, and weight and bias are one value per
+// channel, shared by its T group elements: the norm commutes with the group action.
+//     h = (x - mean) rstd,  rstd = 1 / sqrt(var + eps),  y = gamma[c] h + beta[c]
+// Backward, with g = dy gamma[c]:
+//     dx        = rstd (g - mean(g) - h mean(g h)) [+ dres]
+//     dgamma[c] = sum over rows and t of dy h,   dbeta[c] = sum over rows and t of dy
+// h comes from x and the row's statistics, or from the 8-bit checkpoint of h that the forward
+// pass wrote (eql_ckpt8.h).
+//
+// All of it is bound by memory: one read of each operand, one write of each result.  Rows of up
+// to kNormMaxRow features are held in registers between the two uses (statistics, result): LPR
+// lanes take a row, K chunks of 8 features a lane, chunk j of the row on lane j % LPR.  The
+// variance is the mean square of the centred row, a second pass over registers.  Sums are fp32.
+// A workgroup takes rows 256 / LPR at a time in a grid-stride loop, with gamma and beta, and in
+// the backward pass the column sums of dy h and dy, in registers for the whole loop.
+// Longer rows go through the kernels at the end of this file.
+#pragma once
+
+#include "eql_ckpt8.h"
+
+namespace eql {
+
+struct NormArgs {
+  const void* x;      // [N][R] (backward: unless the checkpoint is read)
+  const void* gamma;  // [C] or null (1)
+  const void* beta;   // [C] or null (0)
+  void* y;            // forward: [N][R]
+  unsigned char* codes;   // checkpoint of h, or null
+  unsigned char* scales;
+  float* mean;        // [N] or null
+  float* rstd;        // [N] or null
+  const void* dy;     // backward: [N][R]
+  const void* dres;   // [N][R] or null
+  void* dx;           // [N][R] (may be dy or dres)
+  float* part;        // [gridDim][2][C] column sums (wide: [rowBlocks][2][R]), or null
+  float* rowSums;     // wide backward: [N][2], mean(g) and mean(g h)
+  int64_t N;
+  int R, C, T, pitch;
+  float eps, invR;
+  int rowsPerBlock, colBlocks;  // wide backward
+};
+
+// Sum over the LPR lanes of a row (LPR <= 64), on every lane.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+  v = dpp_add<kDppXor1>(v);
+  v = dpp_add<kDppXor2>(v);
+  if constexpr (LPR >= 8) v = dpp_add<kDppMirror8>(v);
+  if constexpr (LPR >= 16) v = dpp_add<kDppMirror16>(v);
+  if constexpr (LPR >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  }
+  if constexpr (LPR >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  }
+  return v;
+}
+
+// Sums of M values over the lanes of a row; LPR > 64: over the workgroup's waves through LDS
+// (`red`: M x waves floats, one barrier before the reads; the caller alternates two areas).
+template <int LPR, int M>
+__device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = row_sum<(LPR < 64 ? LPR : 64)>(v[m]);
+  if constexpr (LPR > 64) {
+    constexpr int W = LPR / 64;
+    const int wave = (int)threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) red[m * W + wave] = v[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      float t = red[m * W];
+#pragma unroll
+      for (int w = 1; w < W; ++w) t += red[m * W + w];
+      v[m] = t;
+    }
+  }
+}
+
+// One per-channel parameter spread over the 8 features of a chunk (as elements).
+template <typename Elt>
+__device__ __forceinline__ typename Chunk<Elt>::V spread(const void* p, int f0, int R, int T, float missing) {
+  typename Chunk<Elt>::V v;
+  int c = f0 / T, t = f0 - c * T;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = p && f0 + e < R ? static_cast<const Elt*>(p)[c] : (Elt)missing;
+    if (++t == T) {
+      t = 0;
+      ++c;
+    }
+  }
+  return v;
+}
+
+template <typename Elt, int LPR, int K, bool WHOLE>
+__global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
+  using V = typename Chunk<Elt>::V;
+  constexpr int G = 256 / LPR;
+  __shared__ float red[2][8];
+  const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
+  V gam[K], bet[K];
+  int n[K];  // elements of each chunk
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int f0 = (lane + i * LPR) * 8;
+    n[i] = a.R - f0;
+    gam[i] = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+    bet[i] = spread<Elt>(a.beta, f0, a.R, a.T, 0.0f);
+  }
+  for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += (int64_t)gridDim.x * G) {
+    const int64_t row = base + grp;
+    const bool live = row < a.N;
+    const Elt* xr = static_cast<const Elt*>(a.x) + row * a.R;
+    float v[K][8];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const V u = load_chunk8<Elt, WHOLE>(xr + (lane + i * LPR) * 8, live ? n[i] : 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = (float)u[e];
+        s[0] += v[i][e];
+      }
+    }
+    row_sums<LPR>(s, red[0]);
+    const float mean = s[0] * a.invR;
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = (WHOLE ? n[i] >= 8 : e < n[i]) ? v[i][e] - mean : 0.0f;
+        q[0] = __builtin_fmaf(v[i][e], v[i][e], q[0]);
+      }
+    row_sums<LPR>(q, red[1]);
+    // 1 / sqrt to the last bit or so: the square root and the quotient are correctly rounded.
+    const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(q[0], a.invR, a.eps));
+    if (live && lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int f0 = (lane + i * LPR) * 8;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] *= rstd;
+        o[e] = __builtin_fmaf(v[i][e], (float)gam[i][e], (float)bet[i][e]);
+      }
+      if (live) store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.y) + row * a.R + f0, n[i], o);
+      if (a.codes) {
+        // Past the row's end h is zero, so the codes that pad the last block are too.
+        const uint32_t sc = block_scale(top_bits(v[i]));
+        if (live && f0 < a.pitch) {
+          *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(v[i], sc);
+          if ((lane & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
+        }
+      }
+    }
+  }
+}
+
+// CKPT: h from the checkpoint (codes, scales, rstd), else from x, mean and rstd.
+// Dynamic LDS: [256 / LPR][R] floats, for the column sums at the end.
+template <typename Elt, int LPR, int K, bool WHOLE, bool CKPT>
+__global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
+  using V = typename Chunk<Elt>::V;
+  constexpr int G = 256 / LPR;
+  extern __shared__ float cols[];
+  __shared__ float red[2][8];
+  const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
+  V gam[K];
+  int n[K];
+  float sg[K][8], sb[K][8];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int f0 = (lane + i * LPR) * 8;
+    n[i] = a.R - f0;
+    gam[i] = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += (int64_t)gridDim.x * G) {
+    const int64_t row = base + grp;
+    const bool live = row < a.N;
+    const float rstd = live ? a.rstd[row] : 0.0f;
+    const float mean = !CKPT && live ? a.mean[row] : 0.0f;
+    float h[K][8];
+    V dy[K];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int f0 = (lane + i * LPR) * 8;
+      const int m = live ? n[i] : 0;
+      dy[i] = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.dy) + row * a.R + f0, m);
+      if constexpr (CKPT) {
+        u32x2 w = {0, 0};
+        float step = 0.0f;
+        if (m > 0) {
+          w = *reinterpret_cast<const u32x2*>(a.codes + row * a.pitch + f0);
+          step = scale_step(a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
+        }
+        decode8(w, step, h[i]);
+      } else {
+        const V u = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.x) + row * a.R + f0, m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = ((float)u[e] - mean) * rstd;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // Past the row's end dy is zero, and so are its products (h is finite there only if the
+        // row's statistics are, but such a row is NaN throughout anyway).
+        const float d = (float)dy[i][e];
+        const float g = d * (float)gam[i][e];
+        s[0] += g;
+        s[1] = __builtin_fmaf(g, h[i][e], s[1]);
+        sb[i][e] += d;
+        sg[i][e] = __builtin_fmaf(d, h[i][e], sg[i][e]);
+      }
+    }
+    row_sums<LPR>(s, red[turn]);
+    turn ^= 1;
+    const float m1 = s[0] * a.invR, m2 = s[1] * a.invR;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int f0 = (lane + i * LPR) * 8;
+      const int m = live ? n[i] : 0;
+      V r = zero_chunk<Elt>();
+      if (a.dres) r = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.dres) + row * a.R + f0, m);
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = (float)dy[i][e] * (float)gam[i][e];
+        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, g - m1), (float)r[e]);
+      }
+      store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.dx) + row * a.R + f0, m, o);
+    }
+  }
+  if (!a.part) return;
+  // Column sums: the row groups' sums of each feature through LDS, then per channel its T
+  // features, row group by row group, in a fixed order.
+  float* out = a.part + (int64_t)blockIdx.x * 2 * a.C;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int f0 = (lane + i * LPR) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (f0 + e < a.R) cols[grp * a.R + f0 + e] = which ? sb[i][e] : sg[i][e];
+    }
+    __syncthreads();
+    for (int c = (int)threadIdx.x; c < a.C; c += 256) {
+      float t = 0.0f;
+      for (int q = 0; q < G; ++q)
+        for (int j = 0; j < a.T; ++j) t += cols[q * a.R + c * a.T + j];
+      out[which * a.C + c] = t;
+    }
+  }
+}
+
+// dgamma and dbeta from the blocks' column sums part[b][2][C * F] (F features a channel left to
+// add): a workgroup takes 16 channels x 16 slices of the blocks, slice l blocks l, l + 16, ...;
+// the slices are added in order and the result rounded once.
+struct NormParamArgs {
+  const float* part;
+  void* dgamma;  // [C] or null
+  void* dbeta;   // [C] or null
+  int blocks, C, F, groups;  // groups = ceil(C / 16); workgroups groups .. 2 groups - 1: dbeta
+};
+
+template <typename Elt>
+__global__ void __launch_bounds__(256) eql_norm_param_kernel(const NormParamArgs a) {
+  __shared__ float red[16][17];
+  const bool beta = (int)blockIdx.x >= a.groups;
+  const int c = ((int)blockIdx.x - (beta ? a.groups : 0)) * 16 + ((int)threadIdx.x & 15), sl = (int)threadIdx.x >> 4;
+  void* dst = beta ? a.dbeta : a.dgamma;
+  if (!dst) return;
+  const int64_t stride = (int64_t)a.C * a.F;
+  float s = 0.0f;
+  if (c < a.C) {
+    const float* p = a.part + (beta ? stride : 0) + (int64_t)c * a.F;
+    for (int b = sl; b < a.blocks; b += 16)
+      for (int f = 0; f < a.F; ++f) s += p[b * 2 * stride + f];
+  }
+  red[sl][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (sl == 0 && c < a.C) {
+    float t = red[0][threadIdx.x];
+#pragma unroll
+    for (int l = 1; l < 16; ++l) t += red[l][threadIdx.x];
+    static_cast<Elt*>(dst)[c] = (Elt)t;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows longer than the registers hold.  Forward: a workgroup per row reads it three times
+// (sum, centred squares, result), the second and third time from cache.  Backward: a
+// workgroup per row for the two row means, then a kernel over column blocks and row blocks
+// that writes dx and the column sums.
+// ---------------------------------------------------------------------------
+template <int M>
+__device__ __forceinline__ void block_sums(float (&v)[M], float* red) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = row_sum<64>(v[m]);
+  const int wave = (int)threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) red[m * 16 + wave] = v[m];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    float t = red[m * 16];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) t += red[m * 16 + w];
+    v[m] = t;
+  }
+}
+
+template <typename Elt>
+__global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs a) {
+  __shared__ float red[16];
+  const int64_t row = blockIdx.x;
+  const Elt* xr = static_cast<const Elt*>(a.x) + row * a.R;
+  float s[1] = {0.0f};
+  for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
+    const auto u = load_chunk8<Elt, false>(xr + f0, a.R - f0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] += (float)u[e];
+  }
+  block_sums(s, red);
+  const float mean = s[0] * a.invR;
+  float q[1] = {0.0f};
+  for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
+    const auto u = load_chunk8<Elt, false>(xr + f0, a.R - f0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = f0 + e < a.R ? (float)u[e] - mean : 0.0f;
+      q[0] = __builtin_fmaf(d, d, q[0]);
+    }
+  }
+  block_sums(q, red);
+  const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(q[0], a.invR, a.eps));
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+  // To the end of the row's last block of 32: whole quads stay together for its scale.
+  for (int f0 = (int)threadIdx.x * 8; f0 < a.pitch; f0 += 8192) {
+    const int n = a.R - f0;
+    const auto u = load_chunk8<Elt, false>(xr + f0, n);
+    const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f), bet = spread<Elt>(a.beta, f0, a.R, a.T, 0.0f);
+    float h[8], o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      h[e] = e < n ? ((float)u[e] - mean) * rstd : 0.0f;
+      o[e] = __builtin_fmaf(h[e], (float)gam[e], (float)bet[e]);
+    }
+    store_chunk8<Elt, false>(static_cast<Elt*>(a.y) + row * a.R + f0, n, o);
+    if (a.codes) {
+      const uint32_t sc = block_scale(top_bits(h));
+      *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(h, sc);
+      if ((threadIdx.x & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
+    }
+  }
+}
+
+// h of one chunk, from x or the checkpoint (zero past the row's end).
+template <typename Elt, bool CKPT>
+__device__ __forceinline__ void wide_h(const NormArgs& a, int64_t row, int f0, int n, float mean, float rstd, float (&h)[8]) {
+  if constexpr (CKPT) {
+    const float step = scale_step(a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
+    decode8(*reinterpret_cast<const u32x2*>(a.codes + row * a.pitch + f0), step, h);
+  } else {
+    const auto u = load_chunk8<Elt, false>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = ((float)u[e] - mean) * rstd;
+  }
+}
+
+template <typename Elt, bool CKPT>
+__global__ void __launch_bounds__(1024) eql_norm_bwd_rows_kernel(const NormArgs a) {
+  __shared__ float red[32];
+  const int64_t row = blockIdx.x;
+  const float rstd = a.rstd[row], mean = CKPT ? 0.0f : a.mean[row];
+  float s[2] = {0.0f, 0.0f};
+  for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
+    const int n = a.R - f0;
+    const auto d = load_chunk8<Elt, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
+    const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+    float h[8];
+    wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = (float)d[e] * (float)gam[e];
+      s[0] += g;
+      s[1] = __builtin_fmaf(g, h[e], s[1]);
+    }
+  }
+  block_sums(s, red);
+  if (threadIdx.x < 2) a.rowSums[row * 2 + threadIdx.x] = s[threadIdx.x] * a.invR;
+}
+
+// Workgroup: 256 chunks across (one a lane), rowsPerBlock rows down.
+template <typename Elt, bool CKPT>
+__global__ void __launch_bounds__(256) eql_norm_bwd_cols_kernel(const NormArgs a) {
+  const int cb = (int)blockIdx.x % a.colBlocks, rb = (int)blockIdx.x / a.colBlocks;
+  const int f0 = (cb * 256 + (int)threadIdx.x) * 8;
+  const int n = a.R - f0;
+  if (n <= 0) return;
+  const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+  float sg[8], sb[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sg[e] = sb[e] = 0.0f;
+  const int64_t r0 = (int64_t)rb * a.rowsPerBlock, r1 = min(a.N, r0 + a.rowsPerBlock);
+  for (int64_t row = r0; row < r1; ++row) {
+    const float rstd = a.rstd[row], mean = CKPT ? 0.0f : a.mean[row];
+    const float m1 = a.rowSums[row * 2], m2 = a.rowSums[row * 2 + 1];
+    const auto d = load_chunk8<Elt, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
+    auto r = zero_chunk<Elt>();
+    if (a.dres) r = load_chunk8<Elt, false>(static_cast<const Elt*>(a.dres) + row * a.R + f0, n);
+    float h[8], o[8];
+    wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float dv = (float)d[e], g = dv * (float)gam[e];
+      sb[e] += dv;
+      sg[e] = __builtin_fmaf(dv, h[e], sg[e]);
+      o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[e], m2, g - m1), (float)r[e]);
+    }
+    store_chunk8<Elt, false>(static_cast<Elt*>(a.dx) + row * a.R + f0, n, o);
+  }
+  if (a.part) {
+    float* out = a.part + (int64_t)rb * 2 * a.R + f0;
+    store_chunk8<float, false>(out, n, sg);
+    store_chunk8<float, false>(out + a.R, n, sb);
+  }
+}
+
+}  // namespace eql

@@ -1,0 +1,55 @@
+// Instantiations of the layer norm's backward kernels and of the parameter gradients' sum.
+#include "eql_block.h"
+
+namespace eql {
+
+template <typename Elt, int LPR, bool WHOLE, bool CKPT>
+static const void* bwd_k(int k) {
+  switch (k) {
+    case 1: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 1, WHOLE, CKPT>;
+    case 2: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 2, WHOLE, CKPT>;
+    case 3: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 3, WHOLE, CKPT>;
+    case 4: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 4, WHOLE, CKPT>;
+    default: return nullptr;
+  }
+}
+
+template <typename Elt, bool WHOLE, bool CKPT>
+static const void* bwd_shape(NormShape sh) {
+  return sh.lpr == 16 ? bwd_k<Elt, 16, WHOLE, CKPT>(sh.k)
+                      : (sh.lpr == 64 ? bwd_k<Elt, 64, WHOLE, CKPT>(sh.k) : bwd_k<Elt, 256, WHOLE, CKPT>(sh.k));
+}
+
+template <typename Elt>
+static const void* bwd_fn(NormShape sh, bool whole, bool ckpt) {
+  return ckpt ? (whole ? bwd_shape<Elt, true, true>(sh) : bwd_shape<Elt, false, true>(sh))
+              : (whole ? bwd_shape<Elt, true, false>(sh) : bwd_shape<Elt, false, false>(sh));
+}
+
+hipError_t launch_norm_bwd(bool f16, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s) {
+  const bool whole = a.R % 8 == 0;
+  const void* fn = f16 ? bwd_fn<_Float16>(sh, whole, ckpt) : bwd_fn<float>(sh, whole, ckpt);
+  if (!fn) return hipErrorInvalidValue;
+  void* kargs[] = {const_cast<NormArgs*>(&a)};
+  const size_t lds = a.part ? (size_t)(256 / sh.lpr) * (size_t)a.R * sizeof(float) : 0;
+  return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, lds, s);
+}
+
+template <typename Elt, bool CKPT>
+static hipError_t bwd_wide(const NormArgs& a, unsigned colGrid, hipStream_t s) {
+  const hipError_t e = launch_kernel((const void*)&eql_norm_bwd_rows_kernel<Elt, CKPT>, (unsigned)a.N, a, s, 1024);
+  if (e != hipSuccess) return e;
+  return launch_kernel((const void*)&eql_norm_bwd_cols_kernel<Elt, CKPT>, colGrid, a, s);
+}
+
+hipError_t launch_norm_bwd_wide(bool f16, bool ckpt, const NormArgs& a, unsigned colGrid, hipStream_t s) {
+  return f16 ? (ckpt ? bwd_wide<_Float16, true>(a, colGrid, s) : bwd_wide<_Float16, false>(a, colGrid, s))
+             : (ckpt ? bwd_wide<float, true>(a, colGrid, s) : bwd_wide<float, false>(a, colGrid, s));
+}
+
+hipError_t launch_norm_param(bool f16, const NormParamArgs& a, hipStream_t s) {
+  return launch_kernel(f16 ? (const void*)&eql_norm_param_kernel<_Float16> : (const void*)&eql_norm_param_kernel<float>,
+                       2u * (unsigned)a.groups, a, s);
+}
+
+}  // namespace eql
