@@ -2,6 +2,7 @@
 // eql_block_api.hip and the kernel instantiations, and what it shares with eql_api.hip.
 #pragma once
 
+#include <cstdlib>
 #include "eql_launch.h"
 #include "eql_norm.h"
 
@@ -16,20 +17,21 @@ constexpr int kNormBwdMaxRow = 8192;
 struct NormShape {
   int lpr, k;
 };
-constexpr NormShape norm_shape(int64_t chunks) {
-  const int lpr = chunks <= 16 * 4 ? 16 : (chunks <= 64 * 4 ? 64 : 256);
+inline NormShape norm_shape(int64_t chunks) {
+  static const int f16 = getenv("N16") ? atoi(getenv("N16")) : 32, f64 = getenv("N64") ? atoi(getenv("N64")) : 256;
+  const int lpr = chunks <= f16 ? 16 : (chunks <= f64 ? 64 : 256);
   const int k = (int)((chunks + lpr - 1) / lpr);
   return {lpr, k > 6 ? 8 : (k > 4 ? 6 : k)};
 }
 
-hipError_t launch_ckpt_pack(bool f16, const CkptArgs& a, unsigned grid, hipStream_t s);
-hipError_t launch_ckpt_unpack(bool f16, const CkptArgs& a, unsigned grid, hipStream_t s);
-hipError_t launch_epi8(bool f16, const Epi8Args& a, unsigned grid, hipStream_t s);
+hipError_t launch_ckpt_pack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s);
+hipError_t launch_ckpt_unpack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s);
+hipError_t launch_epi8(bool f16, bool stream, const Epi8Args& a, unsigned grid, hipStream_t s);
 hipError_t launch_spec8_f16(int T, const Spec8Args& a, unsigned grid, hipStream_t s);
 hipError_t launch_spec8_f32(int T, const Spec8Args& a, unsigned grid, hipStream_t s);
-hipError_t launch_norm_fwd(bool f16, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s);
+hipError_t launch_norm_fwd(bool f16, bool stream, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_norm_fwd_wide(bool f16, const NormArgs& a, hipStream_t s);
-hipError_t launch_norm_bwd(bool f16, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s);
+hipError_t launch_norm_bwd(bool f16, bool stream, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_norm_bwd_wide(bool f16, bool ckpt, const NormArgs& a, unsigned colGrid, hipStream_t s);
 hipError_t launch_norm_param(bool f16, const NormParamArgs& a, hipStream_t s);
 

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "eql_block.h"
 #include "eqlinear_block.h"
@@ -19,9 +20,18 @@ bool off(const void* p, uintptr_t to) { return p && reinterpret_cast<uintptr_t>(
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int status_of(hipError_t e) { return e == hipSuccess ? EQL_OK : EQL_EHIP; }
 
+// Passes that move more than the last-level cache holds (256 MB) read their operands past the
+// caches; smaller ones often find them there.
+bool streams(int64_t bytes) { return bytes > (256LL << 20); }
+
 // Workgroups of the norm's grid-stride kernels.
-constexpr int64_t kNormFwdGrid = 2048;
-constexpr int64_t kNormBwdGrid = 1024;
+int64_t genv(const char* n, int64_t d) { const char* e = std::getenv(n); return e ? std::atoll(e) : d; }
+const int64_t kNormFwdGrid = genv("FG", 1024);
+const int64_t kNormBwdGrid = genv("BG", 512);
+
+// Workgroups for `turns` turns of a grid-stride loop: at most `most`, all with the same number
+// of turns or one less.
+int64_t even_grid(int64_t turns, int64_t most) { return ceil_div(turns, ceil_div(turns, most)); }
 
 // Launch shape of the norm's backward.  wide: rows longer than the registers hold.
 struct BwdPlan {
@@ -39,7 +49,7 @@ BwdPlan plan_norm_bwd(int64_t N, int64_t Cp, int T) {
   const int64_t R = Cp * T;
   if (R <= kNormBwdMaxRow) {
     p.shape = norm_shape(ceil_div(R, 8));
-    p.grid = std::min(ceil_div(N, 256 / p.shape.lpr), kNormBwdGrid);
+    p.grid = even_grid(ceil_div(N, 256 / p.shape.lpr), kNormBwdGrid);
     p.partBytes = (size_t)p.grid * 2 * (size_t)Cp * sizeof(float);
     return p;
   }
@@ -109,7 +119,8 @@ int norm_bwd(bool fromCkpt, const void* dy, const void* x, const void* ckpt, con
       a.rowsPerBlock = (int)p.rowsPerBlock;
       e = launch_norm_bwd_wide(f16, fromCkpt, a, (unsigned)(p.rowBlocks * p.colBlocks), s);
     } else {
-      e = launch_norm_bwd(f16, p.shape, fromCkpt, a, (unsigned)p.grid, s);
+      const int64_t moved = elt_bytes(dtype) * (2 + (dres ? 1 : 0)) + (fromCkpt ? 1 : elt_bytes(dtype));
+      e = launch_norm_bwd(f16, streams(N * (int64_t)a.R * moved), p.shape, fromCkpt, a, (unsigned)p.grid, s);
     }
     if (e != hipSuccess) return EQL_EHIP;
   }
@@ -143,8 +154,9 @@ int ckpt_copy(bool pack, const void* x, const void* ckpt, int64_t N, int64_t Cp,
   const int64_t grid = ceil_div(a.chunks, 256);
   if (grid > kMaxGrid) return EQL_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return status_of(pack ? launch_ckpt_pack(dtype == EQL_F16, a, (unsigned)grid, s)
-                        : launch_ckpt_unpack(dtype == EQL_F16, a, (unsigned)grid, s));
+  const bool stream_in = streams(N * (int64_t)a.R * (elt_bytes(dtype) + 1));
+  return status_of(pack ? launch_ckpt_pack(dtype == EQL_F16, stream_in, a, (unsigned)grid, s)
+                        : launch_ckpt_unpack(dtype == EQL_F16, stream_in, a, (unsigned)grid, s));
 }
 
 }  // namespace
@@ -193,8 +205,8 @@ int eqlinear_layernorm_fwd(const void* x, const void* gamma, const void* beta, v
     return status_of(launch_norm_fwd_wide(f16, a, s));
   }
   const NormShape sh = norm_shape(a.pitch / 8);
-  const int64_t grid = std::min(ceil_div(N, 256 / sh.lpr), kNormFwdGrid);
-  return status_of(launch_norm_fwd(f16, sh, a, (unsigned)grid, s));
+  const int64_t grid = even_grid(ceil_div(N, 256 / sh.lpr), kNormFwdGrid);
+  return status_of(launch_norm_fwd(f16, streams(N * (int64_t)a.R * (2 * elt_bytes(dtype) + (ckpt ? 1 : 0))), sh, a, (unsigned)grid, s));
 }
 
 size_t eqlinear_layernorm_bwd_workspace_bytes(int64_t N, int64_t Cp, int T, int dtype) {
@@ -237,17 +249,17 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   a.codes = static_cast<const unsigned char*>(pre_ckpt);
   a.scales = a.codes ? a.codes + N * a.pitch : nullptr;
   a.part = parts ? static_cast<float*>(workspace) : nullptr;
-  // Chunks across a workgroup: the row's chunks spread evenly over as few column blocks of at
-  // most 256 lanes as hold them; a narrow row leaves room for more rows at a time.
+  // Chunks across a workgroup: the row's chunks spread evenly over as few column blocks as hold
+  // them; a narrow row leaves room for more rows at a time.
   const int64_t chunks = ceil_div(a.R, 8);
-  a.colBlocks = (int)ceil_div(chunks, 256);
+  a.colBlocks = (int)ceil_div(chunks, kEpi8Threads);
   a.lanes = (int)ceil_div(chunks, a.colBlocks);
-  a.groups = 256 / a.lanes;
+  a.groups = kEpi8Threads / a.lanes;
   a.rowsPerBlock = (int)rowsPerBlock;
-  if (rowBlocks * a.colBlocks > kMaxGrid) return EQL_EINVAL;
+  if (rowBlocks * a.colBlocks > kMaxGrid / 4) return EQL_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool f16 = dtype == EQL_F16;
-  if (N > 0 && launch_epi8(f16, a, (unsigned)(rowBlocks * a.colBlocks), s) != hipSuccess) return EQL_EHIP;
+  if (N > 0 && launch_epi8(f16, streams(N * (int64_t)a.R * (2 * elt_bytes(dtype) + 1)), a, (unsigned)(rowBlocks * a.colBlocks), s) != hipSuccess) return EQL_EHIP;
   if (!dbias) return EQL_OK;
   EpiBwdArgs b{};
   b.part = a.part;

@@ -47,12 +47,15 @@ __device__ __forceinline__ typename Chunk<Elt>::V zero_chunk() {
 }
 
 // The chunk at p, of which `n` elements exist (the others are zero).  WHOLE: every chunk is
-// whole or missing (R a multiple of 8), so no element-wise tail is compiled.
-template <typename Elt, bool WHOLE>
+// whole or missing (R a multiple of 8), so no element-wise tail is compiled.  STREAM: a
+// non-temporal load, for operands that the caches cannot hold anyway.
+template <typename Elt, bool WHOLE, bool STREAM>
 __device__ __forceinline__ typename Chunk<Elt>::V load_chunk8(const Elt* p, int n) {
   typename Chunk<Elt>::V v = zero_chunk<Elt>();
   if (n >= 8) {
-    v = *reinterpret_cast<const typename Chunk<Elt>::VU*>(p);
+    const auto* q = reinterpret_cast<const typename Chunk<Elt>::VU*>(p);
+    if constexpr (STREAM) v = __builtin_nontemporal_load(q);
+    else v = *q;
   } else if (!WHOLE && n > 0) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
@@ -61,18 +64,36 @@ __device__ __forceinline__ typename Chunk<Elt>::V load_chunk8(const Elt* p, int 
   return v;
 }
 
+// Results are written past the caches: nothing in the same kernel reads them again.
 template <typename Elt, bool WHOLE>
 __device__ __forceinline__ void store_chunk8(Elt* p, int n, const float (&f)[8]) {
   if (n >= 8) {
     typename Chunk<Elt>::VU v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (Elt)f[e];
-    *reinterpret_cast<typename Chunk<Elt>::VU*>(p) = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<typename Chunk<Elt>::VU*>(p));
   } else if (!WHOLE && n > 0) {
 #pragma unroll
     for (int e = 0; e < 7; ++e)
       if (e < n) p[e] = (Elt)f[e];
   }
+}
+
+// Eight codes at p (8-byte aligned: rows of codes are a multiple of 32 bytes).
+template <bool STREAM>
+__device__ __forceinline__ u32x2 load_codes8(const unsigned char* p) {
+  const auto* q = reinterpret_cast<const u32x2*>(p);
+  if constexpr (STREAM) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+
+// A checkpoint is small and, in a small step, soon read again: kept in the caches unless the
+// pass streams.
+template <bool STREAM>
+__device__ __forceinline__ void store_codes8(unsigned char* p, u32x2 w) {
+  auto* q = reinterpret_cast<u32x2*>(p);
+  if constexpr (STREAM) __builtin_nontemporal_store(w, q);
+  else *q = w;
 }
 
 // Cross-lane moves inside a row of 16 lanes (DPP): neighbours 1 and 2 apart in a quad, the
@@ -149,7 +170,6 @@ struct CkptArgs {
 // Flat order over the chunks of all rows (pitch / 8 a row, a multiple of four, so a block's
 // four chunks are four neighbouring lanes).  A workgroup's first chunk is split into row and
 // offset once, in 64 bits; a lane adds its own offset and divides in 32 bits.
-template <typename Elt, bool WHOLE>
 __device__ __forceinline__ void chunk_place(const CkptArgs& a, int64_t first, int o, int64_t& row, int& f0, int& n) {
   const int64_t row0 = first / a.rowChunks;
   const uint32_t rest = (uint32_t)(first - row0 * a.rowChunks) + (uint32_t)o;
@@ -159,41 +179,42 @@ __device__ __forceinline__ void chunk_place(const CkptArgs& a, int64_t first, in
   n = a.R - f0;
 }
 
-template <typename Elt, bool WHOLE>
+template <typename Elt, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(256) eql_ckpt_pack_kernel(const CkptArgs a) {
   const int64_t first = (int64_t)blockIdx.x * 256;
   const int64_t idx = first + threadIdx.x;
   if (idx >= a.chunks) return;  // a multiple of four: a quad is live or not as a whole
   int64_t row;
   int f0, n;
-  chunk_place<Elt, WHOLE>(a, first, (int)threadIdx.x, row, f0, n);
-  const auto v = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
+  chunk_place(a, first, (int)threadIdx.x, row, f0, n);
+  const auto v = load_chunk8<Elt, WHOLE, STREAM>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
   float f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
   const uint32_t s = block_scale(top_bits(f));
-  *reinterpret_cast<u32x2*>(a.codes + idx * 8) = encode8(f, s);
+  store_codes8<STREAM>(a.codes + idx * 8, encode8(f, s));
   if ((threadIdx.x & 3) == 0) a.scales[idx >> 2] = (unsigned char)s;
 }
 
-template <typename Elt, bool WHOLE>
+template <typename Elt, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(256) eql_ckpt_unpack_kernel(const CkptArgs a) {
   const int64_t first = (int64_t)blockIdx.x * 256;
   const int64_t idx = first + threadIdx.x;
   if (idx >= a.chunks) return;
   int64_t row;
   int f0, n;
-  chunk_place<Elt, WHOLE>(a, first, (int)threadIdx.x, row, f0, n);
+  chunk_place(a, first, (int)threadIdx.x, row, f0, n);
   const float step = scale_step(a.scales[idx >> 2]);
   float f[8];
-  decode8(*reinterpret_cast<const u32x2*>(a.codes + idx * 8), step, f);
+  decode8(load_codes8<STREAM>(a.codes + idx * 8), step, f);
   store_chunk8<Elt, WHOLE>(static_cast<Elt*>(const_cast<void*>(a.x)) + row * a.R + f0, n, f);
 }
 
 // Backward of the bias + GELU epilogue with GELU's input read from a checkpoint:
 //     dpre = dy GELU'(value),   part[row block][feature] = sum over the block's rows of dpre.
-// A workgroup takes `lanes` chunks across and 256 / lanes rows at a time down its block of
-// rows; the column sums of its row groups are added in a fixed order through LDS.
+// A workgroup of 1024 threads takes `lanes` chunks across and `groups` = 1024 / lanes rows at a
+// time down its block of rows, the next rows' operands in flight; the column sums of its row
+// groups are added pairwise through LDS.
 struct Epi8Args {
   const void* dy;
   const unsigned char* codes;
@@ -203,44 +224,66 @@ struct Epi8Args {
   int64_t N;
   int R, pitch, lanes, groups, colBlocks, rowsPerBlock;
 };
+constexpr int kEpi8Threads = 1024;
 
-template <typename Elt, bool WHOLE>
-__global__ void __launch_bounds__(256) eql_epi8_kernel(const Epi8Args a) {
-  __shared__ float red[256][9];
+template <typename Elt, bool WHOLE, bool STREAM>
+__global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a) {
+  __shared__ float red[8][kEpi8Threads];
   const int grp = (int)threadIdx.x / a.lanes, l = (int)threadIdx.x - grp * a.lanes;
   const int cb = (int)blockIdx.x % a.colBlocks, rb = (int)blockIdx.x / a.colBlocks;
   const int f0 = (cb * a.lanes + l) * 8;
   const int n = a.R - f0;
   const int64_t r0 = (int64_t)rb * a.rowsPerBlock;
-  const int64_t r1 = min(a.N, r0 + a.rowsPerBlock);
+  const int64_t r1 = grp < a.groups && n > 0 ? min(a.N, r0 + a.rowsPerBlock) : r0;
   float s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = 0.0f;
-  if (grp < a.groups && n > 0) {
-    const Elt* dy = static_cast<const Elt*>(a.dy) + f0;
-    Elt* dpre = static_cast<Elt*>(a.dpre) + f0;
-    for (int64_t r = r0 + grp; r < r1; r += a.groups) {
-      const auto g = load_chunk8<Elt, WHOLE>(dy + r * a.R, n);
-      const u32x2 w = *reinterpret_cast<const u32x2*>(a.codes + r * a.pitch + f0);
-      const float step = scale_step(a.scales[r * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
-      float v[8], d[8];
-      decode8(w, step, v);
+  const Elt* dy = static_cast<const Elt*>(a.dy) + f0;
+  Elt* dpre = static_cast<Elt*>(a.dpre) + f0;
+  auto row_step = [&](const typename Chunk<Elt>::V& g, const u32x2& w, uint32_t sc, int64_t r) __attribute__((always_inline)) {
+    float v[8], d[8];
+    decode8(w, scale_step(sc), v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] = (float)g[e] * gelu_grad(v[e]);
-        s[e] += d[e];
-      }
-      store_chunk8<Elt, WHOLE>(dpre + r * a.R, n, d);
+    for (int e = 0; e < 8; ++e) {
+      d[e] = (float)g[e] * gelu_grad(v[e]);
+      s[e] += d[e];
     }
+    store_chunk8<Elt, WHOLE>(dpre + r * a.R, n, d);
+  };
+  int64_t r = r0 + grp;
+  typename Chunk<Elt>::V g;
+  u32x2 w;
+  uint32_t sc = 0;
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+    g = load_chunk8<Elt, WHOLE, STREAM>(dy + row * a.R, n);
+    w = load_codes8<STREAM>(a.codes + row * a.pitch + f0);
+    sc = a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock];
+  };
+  if (r < r1) load(r);
+  while (r < r1) {
+    const auto g0 = g;
+    const u32x2 w0 = w;
+    const uint32_t sc0 = sc;
+    const int64_t at = r;
+    r += a.groups;
+    if (r < r1) load(r);
+    row_step(g0, w0, sc0, at);
   }
   if (!a.part) return;
+  int half = 1;
+  while (half < a.groups) half *= 2;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) red[threadIdx.x][e] = s[e];
-  __syncthreads();
+  for (int e = 0; e < 8; ++e) red[e][threadIdx.x] = s[e];
+  for (half /= 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (grp < half && grp + half < a.groups) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) red[e][threadIdx.x] += red[e][threadIdx.x + half * a.lanes];
+    }
+  }
   if (grp == 0 && n > 0) {
-    for (int q = 1; q < a.groups; ++q)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += red[q * a.lanes + l][e];
+    for (int e = 0; e < 8; ++e) s[e] = red[e][threadIdx.x];
     store_chunk8<float, WHOLE>(a.part + (int64_t)rb * a.R + f0, n, s);
   }
 }

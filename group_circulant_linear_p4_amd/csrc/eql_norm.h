@@ -85,64 +85,90 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
   }
 }
 
-// One per-channel parameter spread over the 8 features of a chunk (as elements).
+// One per-channel parameter spread over the 8 features of a chunk (as elements).  Common group
+// orders fetch their 8 / T channels at once (for T = 4: one 4-byte load of fp16 where eight
+// would do, 48 loads a lane less at R = 384); T = 8 and 16 have one channel a chunk.
 template <typename Elt>
 __device__ __forceinline__ typename Chunk<Elt>::V spread(const void* p, int f0, int R, int T, float missing) {
-  typename Chunk<Elt>::V v;
-  int c = f0 / T, t = f0 - c * T;
+  typedef Elt E2 __attribute__((ext_vector_type(2), aligned(sizeof(Elt))));
+  typename Chunk<Elt>::V v = (typename Chunk<Elt>::V)(Elt)missing;
+  if (!p || f0 >= R) return v;
+  const Elt* q = static_cast<const Elt*>(p);
+  const bool whole = f0 + 8 <= R;
+  if (T == 4 && whole) {
+    const E2 u = *reinterpret_cast<const E2*>(q + f0 / 4);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] = p && f0 + e < R ? static_cast<const Elt*>(p)[c] : (Elt)missing;
-    if (++t == T) {
-      t = 0;
-      ++c;
+    for (int e = 0; e < 8; ++e) v[e] = u[e / 4];
+  } else if ((T & 7) == 0) {
+    v = (typename Chunk<Elt>::V)q[f0 / T];
+  } else if (T == 1 && whole) {
+    v = *reinterpret_cast<const typename Chunk<Elt>::VU*>(q + f0);
+  } else {
+    int c = f0 / T, t = f0 - c * T;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (f0 + e < R) v[e] = q[c];
+      if (++t == T) {
+        t = 0;
+        ++c;
+      }
     }
   }
   return v;
 }
 
-template <typename Elt, int LPR, int K, bool WHOLE>
+template <typename Elt, int LPR, int K, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
   using V = typename Chunk<Elt>::V;
   constexpr int G = 256 / LPR;
   __shared__ float red[2][8];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
+  const int64_t step = (int64_t)gridDim.x * G;
+  // The row after the one at work is loaded before it is needed.
+  V next[K];
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+    const Elt* xr = static_cast<const Elt*>(a.x) + row * a.R;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int f0 = (lane + i * LPR) * 8;
+      next[i] = load_chunk8<Elt, WHOLE, STREAM>(xr + f0, row < a.N ? a.R - f0 : 0);
+    }
+  };
+  load((int64_t)blockIdx.x * G + grp);
   V gam[K], bet[K];
-  int n[K];  // elements of each chunk
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int f0 = (lane + i * LPR) * 8;
-    n[i] = a.R - f0;
     gam[i] = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
     bet[i] = spread<Elt>(a.beta, f0, a.R, a.T, 0.0f);
   }
-  for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += (int64_t)gridDim.x * G) {
+  for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += step) {
     const int64_t row = base + grp;
     const bool live = row < a.N;
-    const Elt* xr = static_cast<const Elt*>(a.x) + row * a.R;
     float v[K][8];
     float s[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const V u = load_chunk8<Elt, WHOLE>(xr + (lane + i * LPR) * 8, live ? n[i] : 0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] = (float)u[e];
-        s[0] += v[i][e];
-      }
-    }
-    row_sums<LPR>(s, red[0]);
-    const float mean = s[0] * a.invR;
-    float q[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < K; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[i][e] = (WHOLE ? n[i] >= 8 : e < n[i]) ? v[i][e] - mean : 0.0f;
+        v[i][e] = (float)next[i][e];
+        s[0] += v[i][e];
+      }
+    if (base + step < a.N) load(row + step);
+    row_sums<LPR>(s, red[0]);
+    const float mean = s[0] * a.invR;
+    float q[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int n = a.R - (lane + i * LPR) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] = (WHOLE ? n >= 8 : e < n) ? v[i][e] - mean : 0.0f;
         q[0] = __builtin_fmaf(v[i][e], v[i][e], q[0]);
       }
+    }
     row_sums<LPR>(q, red[1]);
-    // 1 / sqrt to the last bit or so: the square root and the quotient are correctly rounded.
+    // The square root and the quotient are correctly rounded.
     const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(q[0], a.invR, a.eps));
     if (live && lane == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -157,12 +183,12 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
         v[i][e] *= rstd;
         o[e] = __builtin_fmaf(v[i][e], (float)gam[i][e], (float)bet[i][e]);
       }
-      if (live) store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.y) + row * a.R + f0, n[i], o);
+      if (live) store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.y) + row * a.R + f0, a.R - f0, o);
       if (a.codes) {
         // Past the row's end h is zero, so the codes that pad the last block are too.
         const uint32_t sc = block_scale(top_bits(v[i]));
         if (live && f0 < a.pitch) {
-          *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(v[i], sc);
+          store_codes8<STREAM>(a.codes + row * a.pitch + f0, encode8(v[i], sc));
           if ((lane & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
         }
       }
@@ -170,53 +196,95 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
   }
 }
 
+// Sum over the lanes of a wave that hold the same chunks (LPR < 64), on all of them.
+template <int LPR>
+__device__ __forceinline__ float group_sum(float v) {
+  static_assert(LPR >= 16, "row groups of 16 lanes or more");
+  if constexpr (LPR <= 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  }
+  if constexpr (LPR <= 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  }
+  return v;
+}
+
+// Copies of a feature's column sum that the end of the backward kernel adds through LDS: one a
+// wave, or one in all where a row takes the whole workgroup.
+__host__ __device__ constexpr int norm_bwd_copies(int lpr) { return lpr > 64 ? 1 : 4; }
+
 // CKPT: h from the checkpoint (codes, scales, rstd), else from x, mean and rstd.
-// Dynamic LDS: [256 / LPR][R] floats, for the column sums at the end.
-template <typename Elt, int LPR, int K, bool WHOLE, bool CKPT>
+// Dynamic LDS: norm_bwd_copies(LPR) * R floats, for the column sums at the end.
+template <typename Elt, int LPR, int K, bool WHOLE, bool STREAM, bool CKPT>
 __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   using V = typename Chunk<Elt>::V;
   constexpr int G = 256 / LPR;
   extern __shared__ float cols[];
   __shared__ float red[2][8];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
+  const int64_t step = (int64_t)gridDim.x * G;
+  // All operands of the row after the one at work are loaded before it is needed: the loop
+  // otherwise waits out the memory's latency once before the row's sums and, for dres, again.
+  V dyN[K], xN[K], rN[K];
+  u32x2 wN[K];
+  uint32_t scN[K];
+  float rstdN = 0.0f, meanN = 0.0f;
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+    const bool live = row < a.N;
+    rstdN = live ? a.rstd[row] : 0.0f;
+    if constexpr (!CKPT) meanN = live ? a.mean[row] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const int f0 = (lane + i * LPR) * 8;
+      const int m = live ? a.R - f0 : 0;
+      dyN[i] = load_chunk8<Elt, WHOLE, STREAM>(static_cast<const Elt*>(a.dy) + row * a.R + f0, m);
+      if constexpr (CKPT) {
+        wN[i] = (u32x2){0, 0};
+        scN[i] = 0;
+        if (m > 0) {
+          wN[i] = load_codes8<STREAM>(a.codes + row * a.pitch + f0);
+          scN[i] = a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock];
+        }
+      } else {
+        xN[i] = load_chunk8<Elt, WHOLE, STREAM>(static_cast<const Elt*>(a.x) + row * a.R + f0, m);
+      }
+      rN[i] = zero_chunk<Elt>();
+      if (a.dres) rN[i] = load_chunk8<Elt, WHOLE, STREAM>(static_cast<const Elt*>(a.dres) + row * a.R + f0, m);
+    }
+  };
+  load((int64_t)blockIdx.x * G + grp);
   V gam[K];
-  int n[K];
   float sg[K][8], sb[K][8];
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const int f0 = (lane + i * LPR) * 8;
-    n[i] = a.R - f0;
-    gam[i] = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+    gam[i] = spread<Elt>(a.gamma, (lane + i * LPR) * 8, a.R, a.T, 1.0f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.0f;
   }
   int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += (int64_t)gridDim.x * G) {
+  for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += step) {
     const int64_t row = base + grp;
     const bool live = row < a.N;
-    const float rstd = live ? a.rstd[row] : 0.0f;
-    const float mean = !CKPT && live ? a.mean[row] : 0.0f;
+    const float rstd = rstdN;
     float h[K][8];
-    V dy[K];
+    V dy[K], r[K];
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const int f0 = (lane + i * LPR) * 8;
-      const int m = live ? n[i] : 0;
-      dy[i] = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.dy) + row * a.R + f0, m);
+      dy[i] = dyN[i];
+      r[i] = rN[i];
       if constexpr (CKPT) {
-        u32x2 w = {0, 0};
-        float step = 0.0f;
-        if (m > 0) {
-          w = *reinterpret_cast<const u32x2*>(a.codes + row * a.pitch + f0);
-          step = scale_step(a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
-        }
-        decode8(w, step, h[i]);
+        decode8(wN[i], scale_step(scN[i]), h[i]);
       } else {
-        const V u = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.x) + row * a.R + f0, m);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = ((float)u[e] - mean) * rstd;
+        for (int e = 0; e < 8; ++e) h[i][e] = ((float)xN[i][e] - meanN) * rstd;
       }
+    }
+    if (base + step < a.N) load(row + step);
+#pragma unroll
+    for (int i = 0; i < K; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         // Past the row's end dy is zero, and so are its products (h is finite there only if the
@@ -228,28 +296,27 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
         sb[i][e] += d;
         sg[i][e] = __builtin_fmaf(d, h[i][e], sg[i][e]);
       }
-    }
     row_sums<LPR>(s, red[turn]);
     turn ^= 1;
     const float m1 = s[0] * a.invR, m2 = s[1] * a.invR;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int f0 = (lane + i * LPR) * 8;
-      const int m = live ? n[i] : 0;
-      V r = zero_chunk<Elt>();
-      if (a.dres) r = load_chunk8<Elt, WHOLE>(static_cast<const Elt*>(a.dres) + row * a.R + f0, m);
       float o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float g = (float)dy[i][e] * (float)gam[i][e];
-        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, g - m1), (float)r[e]);
+        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, g - m1), (float)r[i][e]);
       }
-      store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.dx) + row * a.R + f0, m, o);
+      store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.dx) + row * a.R + f0, live ? a.R - f0 : 0, o);
     }
   }
   if (!a.part) return;
-  // Column sums: the row groups' sums of each feature through LDS, then per channel its T
-  // features, row group by row group, in a fixed order.
+  // Column sums: the row groups of a wave across its lanes, the waves through LDS, then per
+  // channel its T features, in a fixed order.
+  constexpr int COPIES = norm_bwd_copies(LPR);
+  const int copy = LPR > 64 ? 0 : (int)threadIdx.x >> 6;
+  const bool writes = LPR >= 64 || (threadIdx.x & 63) < LPR;
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.C;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -258,14 +325,18 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
     for (int i = 0; i < K; ++i) {
       const int f0 = (lane + i * LPR) * 8;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (f0 + e < a.R) cols[grp * a.R + f0 + e] = which ? sb[i][e] : sg[i][e];
+      for (int e = 0; e < 8; ++e) {
+        float t = which ? sb[i][e] : sg[i][e];
+        if constexpr (LPR < 64) t = group_sum<LPR>(t);
+        if (writes && f0 + e < a.R) cols[copy * a.R + f0 + e] = t;
+      }
     }
     __syncthreads();
     for (int c = (int)threadIdx.x; c < a.C; c += 256) {
       float t = 0.0f;
-      for (int q = 0; q < G; ++q)
-        for (int j = 0; j < a.T; ++j) t += cols[q * a.R + c * a.T + j];
+      for (int j = 0; j < a.T; ++j)
+#pragma unroll
+        for (int q = 0; q < COPIES; ++q) t += cols[q * a.R + c * a.T + j];
       out[which * a.C + c] = t;
     }
   }
@@ -292,8 +363,15 @@ __global__ void __launch_bounds__(256) eql_norm_param_kernel(const NormParamArgs
   float s = 0.0f;
   if (c < a.C) {
     const float* p = a.part + (beta ? stride : 0) + (int64_t)c * a.F;
-    for (int b = sl; b < a.blocks; b += 16)
-      for (int f = 0; f < a.F; ++f) s += p[b * 2 * stride + f];
+    // Eight blocks' loads in flight.
+    for (int b = sl; b < a.blocks; b += 128)
+      for (int f = 0; f < a.F; ++f) {
+        float t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) t[u] = b + 16 * u < a.blocks ? p[(b + 16 * u) * 2 * stride + f] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += t[u];
+      }
   }
   red[sl][threadIdx.x & 15] = s;
   __syncthreads();
@@ -338,7 +416,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
   const Elt* xr = static_cast<const Elt*>(a.x) + row * a.R;
   float s[1] = {0.0f};
   for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
-    const auto u = load_chunk8<Elt, false>(xr + f0, a.R - f0);
+    const auto u = load_chunk8<Elt, false, false>(xr + f0, a.R - f0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[0] += (float)u[e];
   }
@@ -346,7 +424,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
   const float mean = s[0] * a.invR;
   float q[1] = {0.0f};
   for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
-    const auto u = load_chunk8<Elt, false>(xr + f0, a.R - f0);
+    const auto u = load_chunk8<Elt, false, false>(xr + f0, a.R - f0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float d = f0 + e < a.R ? (float)u[e] - mean : 0.0f;
@@ -362,7 +440,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
   // To the end of the row's last block of 32: whole quads stay together for its scale.
   for (int f0 = (int)threadIdx.x * 8; f0 < a.pitch; f0 += 8192) {
     const int n = a.R - f0;
-    const auto u = load_chunk8<Elt, false>(xr + f0, n);
+    const auto u = load_chunk8<Elt, false, false>(xr + f0, n);
     const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f), bet = spread<Elt>(a.beta, f0, a.R, a.T, 0.0f);
     float h[8], o[8];
 #pragma unroll
@@ -373,7 +451,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
     store_chunk8<Elt, false>(static_cast<Elt*>(a.y) + row * a.R + f0, n, o);
     if (a.codes) {
       const uint32_t sc = block_scale(top_bits(h));
-      *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(h, sc);
+      store_codes8<false>(a.codes + row * a.pitch + f0, encode8(h, sc));
       if ((threadIdx.x & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
     }
   }
@@ -384,9 +462,9 @@ template <typename Elt, bool CKPT>
 __device__ __forceinline__ void wide_h(const NormArgs& a, int64_t row, int f0, int n, float mean, float rstd, float (&h)[8]) {
   if constexpr (CKPT) {
     const float step = scale_step(a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
-    decode8(*reinterpret_cast<const u32x2*>(a.codes + row * a.pitch + f0), step, h);
+    decode8(load_codes8<false>(a.codes + row * a.pitch + f0), step, h);
   } else {
-    const auto u = load_chunk8<Elt, false>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
+    const auto u = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = ((float)u[e] - mean) * rstd;
   }
@@ -400,7 +478,7 @@ __global__ void __launch_bounds__(1024) eql_norm_bwd_rows_kernel(const NormArgs 
   float s[2] = {0.0f, 0.0f};
   for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
     const int n = a.R - f0;
-    const auto d = load_chunk8<Elt, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
+    const auto d = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
     const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
     float h[8];
     wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
@@ -430,9 +508,9 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_cols_kernel(const NormArgs a
   for (int64_t row = r0; row < r1; ++row) {
     const float rstd = a.rstd[row], mean = CKPT ? 0.0f : a.mean[row];
     const float m1 = a.rowSums[row * 2], m2 = a.rowSums[row * 2 + 1];
-    const auto d = load_chunk8<Elt, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
+    const auto d = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
     auto r = zero_chunk<Elt>();
-    if (a.dres) r = load_chunk8<Elt, false>(static_cast<const Elt*>(a.dres) + row * a.R + f0, n);
+    if (a.dres) r = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dres) + row * a.R + f0, n);
     float h[8], o[8];
     wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
 #pragma unroll

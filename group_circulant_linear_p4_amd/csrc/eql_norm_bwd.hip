@@ -3,35 +3,36 @@
 
 namespace eql {
 
-template <typename Elt, int LPR, bool WHOLE, bool CKPT>
+template <typename Elt, int LPR, bool WHOLE, bool STREAM, bool CKPT>
 static const void* bwd_k(int k) {
   switch (k) {
-    case 1: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 1, WHOLE, CKPT>;
-    case 2: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 2, WHOLE, CKPT>;
-    case 3: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 3, WHOLE, CKPT>;
-    case 4: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 4, WHOLE, CKPT>;
+    case 1: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 1, WHOLE, STREAM, CKPT>;
+    case 2: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 2, WHOLE, STREAM, CKPT>;
+    case 3: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 3, WHOLE, STREAM, CKPT>;
+    case 4: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 4, WHOLE, STREAM, CKPT>;
     default: return nullptr;
   }
 }
 
-template <typename Elt, bool WHOLE, bool CKPT>
+template <typename Elt, bool WHOLE, bool STREAM, bool CKPT>
 static const void* bwd_shape(NormShape sh) {
-  return sh.lpr == 16 ? bwd_k<Elt, 16, WHOLE, CKPT>(sh.k)
-                      : (sh.lpr == 64 ? bwd_k<Elt, 64, WHOLE, CKPT>(sh.k) : bwd_k<Elt, 256, WHOLE, CKPT>(sh.k));
+  return sh.lpr == 16 ? bwd_k<Elt, 16, WHOLE, STREAM, CKPT>(sh.k)
+                      : (sh.lpr == 64 ? bwd_k<Elt, 64, WHOLE, STREAM, CKPT>(sh.k) : bwd_k<Elt, 256, WHOLE, STREAM, CKPT>(sh.k));
 }
 
-template <typename Elt>
-static const void* bwd_fn(NormShape sh, bool whole, bool ckpt) {
-  return ckpt ? (whole ? bwd_shape<Elt, true, true>(sh) : bwd_shape<Elt, false, true>(sh))
-              : (whole ? bwd_shape<Elt, true, false>(sh) : bwd_shape<Elt, false, false>(sh));
+template <typename Elt, bool CKPT>
+static const void* bwd_fn(NormShape sh, bool whole, bool stream) {
+  return whole ? (stream ? bwd_shape<Elt, true, true, CKPT>(sh) : bwd_shape<Elt, true, false, CKPT>(sh))
+               : (stream ? bwd_shape<Elt, false, true, CKPT>(sh) : bwd_shape<Elt, false, false, CKPT>(sh));
 }
 
-hipError_t launch_norm_bwd(bool f16, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s) {
+hipError_t launch_norm_bwd(bool f16, bool stream, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s) {
   const bool whole = a.R % 8 == 0;
-  const void* fn = f16 ? bwd_fn<_Float16>(sh, whole, ckpt) : bwd_fn<float>(sh, whole, ckpt);
+  const void* fn = f16 ? (ckpt ? bwd_fn<_Float16, true>(sh, whole, stream) : bwd_fn<_Float16, false>(sh, whole, stream))
+                       : (ckpt ? bwd_fn<float, true>(sh, whole, stream) : bwd_fn<float, false>(sh, whole, stream));
   if (!fn) return hipErrorInvalidValue;
   void* kargs[] = {const_cast<NormArgs*>(&a)};
-  const size_t lds = a.part ? (size_t)(256 / sh.lpr) * (size_t)a.R * sizeof(float) : 0;
+  const size_t lds = a.part ? (size_t)norm_bwd_copies(sh.lpr) * (size_t)a.R * sizeof(float) : 0;
   return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, lds, s);
 }
 

@@ -3,30 +3,34 @@
 
 namespace eql {
 
-template <typename Elt, int LPR, bool WHOLE>
+template <typename Elt, int LPR, bool WHOLE, bool STREAM>
 static const void* fwd_k(int k) {
   if constexpr (LPR == 256) {
-    if (k == 6) return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 6, WHOLE>;
-    if (k == 8) return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 8, WHOLE>;
+    if (k == 6) return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 6, WHOLE, STREAM>;
+    if (k == 8) return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 8, WHOLE, STREAM>;
   }
   switch (k) {
-    case 1: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 1, WHOLE>;
-    case 2: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 2, WHOLE>;
-    case 3: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 3, WHOLE>;
-    case 4: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 4, WHOLE>;
+    case 1: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 1, WHOLE, STREAM>;
+    case 2: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 2, WHOLE, STREAM>;
+    case 3: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 3, WHOLE, STREAM>;
+    case 4: return (const void*)&eql_norm_fwd_kernel<Elt, LPR, 4, WHOLE, STREAM>;
     default: return nullptr;
   }
 }
 
-template <typename Elt, bool WHOLE>
+template <typename Elt, bool WHOLE, bool STREAM>
 static const void* fwd_shape(NormShape sh) {
-  return sh.lpr == 16 ? fwd_k<Elt, 16, WHOLE>(sh.k) : (sh.lpr == 64 ? fwd_k<Elt, 64, WHOLE>(sh.k) : fwd_k<Elt, 256, WHOLE>(sh.k));
+  return sh.lpr == 16 ? fwd_k<Elt, 16, WHOLE, STREAM>(sh.k) : (sh.lpr == 64 ? fwd_k<Elt, 64, WHOLE, STREAM>(sh.k) : fwd_k<Elt, 256, WHOLE, STREAM>(sh.k));
 }
 
-hipError_t launch_norm_fwd(bool f16, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s) {
-  const bool whole = a.R % 8 == 0;
-  const void* fn = f16 ? (whole ? fwd_shape<_Float16, true>(sh) : fwd_shape<_Float16, false>(sh))
-                       : (whole ? fwd_shape<float, true>(sh) : fwd_shape<float, false>(sh));
+template <typename Elt>
+static const void* fwd_fn(NormShape sh, bool whole, bool stream) {
+  return whole ? (stream ? fwd_shape<Elt, true, true>(sh) : fwd_shape<Elt, true, false>(sh))
+               : (stream ? fwd_shape<Elt, false, true>(sh) : fwd_shape<Elt, false, false>(sh));
+}
+
+hipError_t launch_norm_fwd(bool f16, bool stream, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s) {
+  const void* fn = f16 ? fwd_fn<_Float16>(sh, a.R % 8 == 0, stream) : fwd_fn<float>(sh, a.R % 8 == 0, stream);
   return fn ? launch_kernel(fn, grid, a, s) : hipErrorInvalidValue;
 }
 
