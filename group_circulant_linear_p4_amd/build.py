@@ -44,6 +44,7 @@ SOURCES = [
     "eql_block_api.hip",
     "eql_ckpt8.hip",
     "eql_spec8.hip",
+    "eql_spec8_f32.hip",
     "eql_norm_fwd.hip",
     "eql_norm_bwd.hip",
 ]

@@ -520,10 +520,13 @@ int check_view(const host::CkptView& v, int64_t N, int dtype) {
   return EQL_OK;
 }
 
-// The half spectrum of a checkpointed N x K matrix into operand units, as run_spec's.
+// The half spectrum of a checkpointed N x K matrix into operand units, as run_spec's, and with
+// dy also dy's (K2 channels) in the same launch.
 int run_spec8(const host::CkptView& v, void* out, int64_t N, int64_t K, int64_t Kpad, int64_t kgCount, int T, int dtype,
-              hipStream_t s) {
-  const int64_t grid = ceil_div(kgCount * 2 * Kpad, 256);
+              hipStream_t s, const void* dy = nullptr, void* outDy = nullptr, int64_t K2 = 0, int64_t Kpad2 = 0) {
+  const auto grid_of = [&](int64_t pad) { return ceil_div(kgCount * 2 * pad, 256 * kSpec8Turn) * kSpec8Turn; };
+  const int64_t grid2 = dy ? grid_of(Kpad2) : 0;
+  const int64_t grid = grid2 + grid_of(Kpad);
   if (grid > kMaxGrid) return EQL_EINVAL;
   Spec8Args a{};
   a.pitch = (int)ckpt_pitch(K * T);
@@ -531,14 +534,20 @@ int run_spec8(const host::CkptView& v, void* out, int64_t N, int64_t K, int64_t 
   a.scales = a.codes + N * a.pitch;
   a.gamma = v.gamma;
   a.beta = v.beta;
-  a.act = v.act;
   a.out = out;
   a.N = (int)N;
   a.K = (int)K;
   a.Kpad = (int)Kpad;
   a.kgCount = (int)kgCount;
   a.tw = make_twiddles(T);
-  return status_of(dtype == EQL_F16 ? launch_spec8_f16(T, a, (unsigned)grid, s) : launch_spec8_f32(T, a, (unsigned)grid, s));
+  a.m2 = dy;
+  a.out2 = outDy;
+  a.K2 = (int)K2;
+  a.Kpad2 = (int)Kpad2;
+  a.blocks1 = (int)grid2;
+  const int view = v.act == EQL_ACT_GELU ? kViewGelu : (v.gamma || v.beta ? kViewAffine : kViewPlain);
+  return status_of(dtype == EQL_F16 ? launch_spec8_f16(T, view, a, (unsigned)grid, s)
+                                    : launch_spec8_f32(T, view, a, (unsigned)grid, s));
 }
 
 // Body of the weight-gradient entry points.  spectra: the workspace already holds x's
@@ -597,8 +606,7 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
   } else if (N > 0) {
     hipError_t e = hipSuccess;
     if (view) {
-      st = run_spec8(*view, ws + p.dyhBytes, N, Cp, p.Cpad, p.kgCount, T, dtype, s);
-      if (st == EQL_OK) st = run_spec(dy, ws, N, Dp, p.Dpad, p.kgCount, T, dtype, s);
+      st = run_spec8(*view, ws + p.dyhBytes, N, Cp, p.Cpad, p.kgCount, T, dtype, s, dy, ws, Dp, p.Dpad);
       if (st != EQL_OK) return st;
     } else if (!spectra) {
       // dy's and x's spectra in one launch: dy's workgroups first, then x's.
@@ -618,10 +626,10 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
       e = f16 ? launch_spec_f16(T, sp, (unsigned)(gdy + gx), s) : launch_spec_f32(T, sp, (unsigned)(gdy + gx), s);
       if (e != hipSuccess) return EQL_EHIP;
     }
+    BwdwArgs gemm[2];
     for (int pair = 0; pair < 2; ++pair) {
       const GemmPlan& g = pair ? p.pair : p.real;
-      if (g.items() == 0) continue;
-      BwdwArgs a{};
+      BwdwArgs& a = gemm[pair] = BwdwArgs{};
       a.dyh = ws;
       a.xh = ws + p.dyhBytes;
       a.ws = pair ? partP : partR;
@@ -635,13 +643,24 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
       a.dTiles = (int)g.dTiles;
       a.cTiles = (int)g.cTiles;
       a.numItems = (int)g.items();
-      if (pair)
-        e = f16 ? launch_bwdw_pair_f16(T, g.DB, g.CB, g.WCN, a, (unsigned)a.numItems, s)
-                : launch_bwdw_pair_f32(T, g.DB, g.CB, g.WCN, a, (unsigned)a.numItems, s);
-      else
-        e = f16 ? launch_bwdw_real_f16(T, g.DB, g.CB, g.WCN, a, (unsigned)a.numItems, s)
-                : launch_bwdw_real_f32(T, g.DB, g.CB, g.WCN, a, (unsigned)a.numItems, s);
+    }
+    const auto small = [](const GemmPlan& g) { return g.items() > 0 && g.DB == 1 && g.CB == 1 && g.WCN == 2; };
+    if (small(p.real) && small(p.pair) && p.real.items() + p.pair.items() <= kMaxGrid) {
+      e = f16 ? launch_bwdw_both_f16(T, gemm[1], gemm[0], s) : launch_bwdw_both_f32(T, gemm[1], gemm[0], s);
       if (e != hipSuccess) return EQL_EHIP;
+    } else {
+      if (p.real.items() > 0) {
+        const GemmPlan& g = p.real;
+        e = f16 ? launch_bwdw_real_f16(T, g.DB, g.CB, g.WCN, gemm[0], (unsigned)gemm[0].numItems, s)
+                : launch_bwdw_real_f32(T, g.DB, g.CB, g.WCN, gemm[0], (unsigned)gemm[0].numItems, s);
+        if (e != hipSuccess) return EQL_EHIP;
+      }
+      if (p.pair.items() > 0) {
+        const GemmPlan& g = p.pair;
+        e = f16 ? launch_bwdw_pair_f16(T, g.DB, g.CB, g.WCN, gemm[1], (unsigned)gemm[1].numItems, s)
+                : launch_bwdw_pair_f32(T, g.DB, g.CB, g.WCN, gemm[1], (unsigned)gemm[1].numItems, s);
+        if (e != hipSuccess) return EQL_EHIP;
+      }
     }
   }
   BwdwReduceArgs r{};

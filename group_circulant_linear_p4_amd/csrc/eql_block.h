@@ -2,7 +2,6 @@
 // eql_block_api.hip and the kernel instantiations, and what it shares with eql_api.hip.
 #pragma once
 
-#include <cstdlib>
 #include "eql_launch.h"
 #include "eql_norm.h"
 
@@ -13,13 +12,14 @@ constexpr int kNormFwdMaxRow = 16384;
 constexpr int kNormBwdMaxRow = 8192;
 
 // Lanes per row of the register-resident norm kernels and chunks per lane, for rows of `chunks`
-// 8-feature chunks.
+// 8-feature chunks.  A whole wave for a row from 33 chunks on: at N = 16384, R = 512 fp32 one
+// chunk on each of 64 lanes takes 25 us backward where four on each of 16 take 29, and at N =
+// 197, R = 384 fp16 3.3 us forward where three on each of 16 take 4.4.
 struct NormShape {
   int lpr, k;
 };
-inline NormShape norm_shape(int64_t chunks) {
-  static const int f16 = getenv("N16") ? atoi(getenv("N16")) : 32, f64 = getenv("N64") ? atoi(getenv("N64")) : 256;
-  const int lpr = chunks <= f16 ? 16 : (chunks <= f64 ? 64 : 256);
+constexpr NormShape norm_shape(int64_t chunks) {
+  const int lpr = chunks <= 32 ? 16 : (chunks <= 64 * 4 ? 64 : 256);
   const int k = (int)((chunks + lpr - 1) / lpr);
   return {lpr, k > 6 ? 8 : (k > 4 ? 6 : k)};
 }
@@ -27,8 +27,8 @@ inline NormShape norm_shape(int64_t chunks) {
 hipError_t launch_ckpt_pack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_ckpt_unpack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_epi8(bool f16, bool stream, const Epi8Args& a, unsigned grid, hipStream_t s);
-hipError_t launch_spec8_f16(int T, const Spec8Args& a, unsigned grid, hipStream_t s);
-hipError_t launch_spec8_f32(int T, const Spec8Args& a, unsigned grid, hipStream_t s);
+hipError_t launch_spec8_f16(int T, int view, const Spec8Args& a, unsigned grid, hipStream_t s);
+hipError_t launch_spec8_f32(int T, int view, const Spec8Args& a, unsigned grid, hipStream_t s);
 hipError_t launch_norm_fwd(bool f16, bool stream, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_norm_fwd_wide(bool f16, const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(bool f16, bool stream, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s);

@@ -66,15 +66,13 @@ struct BwdwReduceArgs {
   Twiddles tw;
 };
 
+// Thread `idx` of one matrix's transform: channel idx % Kpad, half and k-step above it.
 template <int T, typename Elt>
-__global__ void __launch_bounds__(256) eql_spec_kernel(const SpecArgs a) {
+__device__ __forceinline__ void spec_thread(const Elt* m, void* outUnits, int N, int K, int Kpad, int kgCount, size_t idx,
+                                            const Twiddles& tw) {
   using E = EltT<Elt>;
   constexpr int G = E::kPerUnit;
-  const bool second = (int)blockIdx.x >= a.blocks1;
-  const Elt* const m = static_cast<const Elt*>(second ? a.m2 : a.m);
-  const int K = second ? a.K2 : a.K, Kpad = second ? a.Kpad2 : a.Kpad;
-  const size_t idx = (size_t)((int)blockIdx.x - (second ? a.blocks1 : 0)) * 256 + threadIdx.x;
-  if (idx >= (size_t)a.kgCount * 2 * Kpad) return;
+  if (idx >= (size_t)kgCount * 2 * Kpad) return;
   const int k = (int)(idx % Kpad);
   const size_t rest = idx / Kpad;
   const int half = (int)(rest & 1);
@@ -85,25 +83,34 @@ __global__ void __launch_bounds__(256) eql_spec_kernel(const SpecArgs a) {
   for (int e = 0; e < G; ++e) {
     float v[T], o[T];
     const int row = row0 + e;
-    if (row < a.N && k < K) {
+    if (row < N && k < K) {
       load_group<T, Elt>(m + ((size_t)row * K + k) * T, v);
     } else {
 #pragma unroll
       for (int h = 0; h < T; ++h) v[h] = 0.0f;
     }
-    Dft<T>::run(v, o, a.tw);
+    Dft<T>::run(v, o, tw);
 #pragma unroll
     for (int p = 0; p < T; ++p) pl[p][e] = o[p];
   }
   // Non-temporal: the spectra are read back by the GEMMs only after the whole
   // transform, long after they would have left the caches.
-  u32x4* out = static_cast<u32x4*>(second ? a.out2 : a.out) + ((size_t)kg * T * 2 + half) * Kpad + k;
+  u32x4* out = static_cast<u32x4*>(outUnits) + ((size_t)kg * T * 2 + half) * Kpad + k;
 #pragma unroll
   for (int p = 0; p < T; ++p) __builtin_nontemporal_store(E::pack(pl[p]), &out[(size_t)p * 2 * Kpad]);
 }
 
+template <int T, typename Elt>
+__global__ void __launch_bounds__(256) eql_spec_kernel(const SpecArgs a) {
+  const bool second = (int)blockIdx.x >= a.blocks1;
+  const size_t idx = (size_t)((int)blockIdx.x - (second ? a.blocks1 : 0)) * 256 + threadIdx.x;
+  spec_thread<T, Elt>(static_cast<const Elt*>(second ? a.m2 : a.m), second ? a.out2 : a.out, a.N, second ? a.K2 : a.K,
+                      second ? a.Kpad2 : a.Kpad, a.kgCount, idx, a.tw);
+}
+
+// One item, as workgroup `block` of a launch of a.numItems.
 template <int T, typename Elt, bool PAIR, int DB, int CB, int WCN>
-__global__ void __launch_bounds__(128 * WCN) eql_bwdw_gemm(const BwdwArgs a) {
+__device__ __forceinline__ void bwdw_gemm_item(const BwdwArgs a, const int block) {
 #if defined(__HIP_DEVICE_COMPILE__)
   using E = EltT<Elt>;
   constexpr int NR = n_real_planes(T);
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(128 * WCN) eql_bwdw_gemm(const BwdwArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wd = wave / WCN, wc = wave % WCN;  // 2 x WCN waves
   const int lcol = lane & 31, khalf = lane >> 5;
-  const int item = xcd_remap(blockIdx.x, a.numItems);
+  const int item = xcd_remap(block, a.numItems);
   const int per = a.groups * a.dTiles * a.cTiles;
   const int split = item / per;
   int rest = item - split * per;
@@ -310,6 +317,24 @@ __global__ void __launch_bounds__(128 * WCN) eql_bwdw_gemm(const BwdwArgs a) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+template <int T, typename Elt, bool PAIR, int DB, int CB, int WCN>
+__global__ void __launch_bounds__(128 * WCN) eql_bwdw_gemm(const BwdwArgs a) {
+  bwdw_gemm_item<T, Elt, PAIR, DB, CB, WCN>(a, (int)blockIdx.x);
+}
+
+// Both plane kinds on 64 x 64 tiles in one launch, the complex pairs' workgroups (twice the
+// work a k-step) first.  Such layers give each launch about one workgroup of four waves per
+// compute unit, each waiting out its own loads; together they fill one another's gaps (C8 fp32,
+// 16384 rows, 64 x 64 channels: 19.1 and 7.7 us in two launches, 21.8 in one).
+template <int T, typename Elt>
+__global__ void __launch_bounds__(256) eql_bwdw_gemm_both(const BwdwArgs pair, const BwdwArgs real) {
+  if ((int)blockIdx.x < pair.numItems) {
+    bwdw_gemm_item<T, Elt, true, 1, 1, 2>(pair, (int)blockIdx.x);
+  } else {
+    bwdw_gemm_item<T, Elt, false, 1, 1, 2>(real, (int)blockIdx.x - pair.numItems);
+  }
+}
+
 // Sum of the split partials, then the inverse group transform.  WAVES = 1: one
 // output per thread, all splits in one chain.  WAVES = 4 or 16 (for long chains):
 // a workgroup covers 256 / WAVES consecutive (d, c) outputs, and the threads of
@@ -325,6 +350,10 @@ __global__ void __launch_bounds__(256) eql_bwdw_reduce(const BwdwReduceArgs a) {
   constexpr int NR = n_real_planes(T);
   constexpr int NC = T - NR;  // planes of the complex pairs
   constexpr int OUTS = 256 / WAVES;
+  // Four phases share chains of about a dozen splits: four of them in flight (the p4 fp16 layer
+  // with 96 x 384 channels and 12608 rows: 9.3 -> 6.2 us).  Chains of five to eight (16 phases) or
+  // one phase of long streams lose by it (7.4 -> 10.3 us and 24 -> 27 us).
+  constexpr int UNROLL = WAVES == 4 ? 4 : 1;
   __shared__ float part[WAVES > 1 ? WAVES - 1 : 1][T][OUTS];
   const int lane = threadIdx.x % OUTS, w = threadIdx.x / OUTS;
   const size_t idx = (size_t)blockIdx.x * OUTS + lane;
@@ -334,11 +363,13 @@ __global__ void __launch_bounds__(256) eql_bwdw_reduce(const BwdwReduceArgs a) {
 #pragma unroll
   for (int p = 0; p < T; ++p) P[p] = 0.0f;
   if (live) {
+#pragma unroll(UNROLL)
     for (int s = w; s < a.SR; s += WAVES) {
 #pragma unroll
       for (int p = 0; p < NR; ++p) P[p] += a.wsR[((size_t)s * NR + p) * plane + idx];
     }
     if constexpr (NC > 0) {
+#pragma unroll(UNROLL)
       for (int s = w; s < a.SP; s += WAVES) {
 #pragma unroll
         for (int p = 0; p < NC; ++p) P[NR + p] += a.wsP[((size_t)s * NC + p) * plane + idx];

@@ -23,4 +23,21 @@ hipError_t launch_bwdw_pair_f32(int T, int DB, int CB, int WCN, const BwdwArgs& 
 #undef EQL_CASE
 }
 
+template <int T>
+static hipError_t both_one(const BwdwArgs& pair, const BwdwArgs& real, hipStream_t s) {
+  if constexpr (n_pairs(T) == 0) {
+    return hipErrorInvalidValue;
+  } else {
+    void* kargs[] = {const_cast<BwdwArgs*>(&pair), const_cast<BwdwArgs*>(&real)};
+    return hipLaunchKernel((const void*)&eql_bwdw_gemm_both<T, float>, dim3((unsigned)(pair.numItems + real.numItems)),
+                           dim3(256), kargs, 0, s);
+  }
+}
+
+hipError_t launch_bwdw_both_f32(int T, const BwdwArgs& pair, const BwdwArgs& real, hipStream_t s) {
+#define EQL_CASE(t) return both_one<t>(pair, real, s);
+  EQL_FOR_EACH_T(T, EQL_CASE)
+#undef EQL_CASE
+}
+
 }  // namespace eql

@@ -64,7 +64,10 @@ __device__ __forceinline__ typename Chunk<Elt>::V load_chunk8(const Elt* p, int 
   return v;
 }
 
-// Results are written past the caches: nothing in the same kernel reads them again.
+// Results are written past the caches, 16 bytes a lane: nothing in the same kernel reads them
+// again.  (Codes, 8 bytes a lane, are not: as non-temporal stores they took the norm's forward
+// pass with its checkpoint at N = 65536, R = 4096 from 228 to 273 us, and a small step soon
+// reads them again.)
 template <typename Elt, bool WHOLE>
 __device__ __forceinline__ void store_chunk8(Elt* p, int n, const float (&f)[8]) {
   if (n >= 8) {
@@ -85,15 +88,6 @@ __device__ __forceinline__ u32x2 load_codes8(const unsigned char* p) {
   const auto* q = reinterpret_cast<const u32x2*>(p);
   if constexpr (STREAM) return __builtin_nontemporal_load(q);
   else return *q;
-}
-
-// A checkpoint is small and, in a small step, soon read again: kept in the caches unless the
-// pass streams.
-template <bool STREAM>
-__device__ __forceinline__ void store_codes8(unsigned char* p, u32x2 w) {
-  auto* q = reinterpret_cast<u32x2*>(p);
-  if constexpr (STREAM) __builtin_nontemporal_store(w, q);
-  else *q = w;
 }
 
 // Cross-lane moves inside a row of 16 lanes (DPP): neighbours 1 and 2 apart in a quad, the
@@ -192,7 +186,7 @@ __global__ void __launch_bounds__(256) eql_ckpt_pack_kernel(const CkptArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
   const uint32_t s = block_scale(top_bits(f));
-  store_codes8<STREAM>(a.codes + idx * 8, encode8(f, s));
+  *reinterpret_cast<u32x2*>(a.codes + idx * 8) = encode8(f, s);
   if ((threadIdx.x & 3) == 0) a.scales[idx >> 2] = (unsigned char)s;
 }
 
@@ -289,60 +283,96 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
 }
 
 // x's half spectrum for the weight gradient, as eql_spec_kernel writes it, with the layer's
-// input rebuilt from a checkpoint: v = act(gamma[c] value + beta[c]).
+// input rebuilt from a checkpoint: v = act(gamma[c] value + beta[c]).  The same launch can
+// transform dy, in blocks1 of its workgroups.
 struct Spec8Args {
   const unsigned char* codes;
   const unsigned char* scales;
   const void* gamma;  // [K] or null
   const void* beta;   // [K] or null
   void* out;          // units [kgCount][T][2][Kpad]
-  int N, K, Kpad, kgCount, pitch, act;
+  int N, K, Kpad, kgCount, pitch;
   Twiddles tw;
+  const void* m2;     // dy [N][K2*T]
+  void* out2;         // units [kgCount][T][2][Kpad2]
+  int K2, Kpad2, blocks1;
 };
 
-template <int T, typename Elt>
+// What a checkpoint's values become on the way into the layer.  A GELU costs the transform 21
+// operations a feature of about 30; a kernel of its own keeps the other views free of it.
+constexpr int kSpec8Turn = 64;  // both matrices' workgroups are rounded up to this
+enum Ckpt8View { kViewPlain = 0, kViewAffine = 1, kViewGelu = 2 };
+
+template <int T, typename Elt, int VIEW>
 __global__ void __launch_bounds__(256) eql_spec8_kernel(const Spec8Args a) {
   using E = EltT<Elt>;
   constexpr int G = E::kPerUnit;
-  const size_t idx = (size_t)blockIdx.x * 256 + threadIdx.x;
+  // dy's workgroups are spread evenly among x's, kSpec8Turn at a time (every XCD gets both
+  // kinds): those move memory, these compute.
+  const uint32_t turn = blockIdx.x / kSpec8Turn, turns = gridDim.x / kSpec8Turn, dyTurns = a.blocks1 / kSpec8Turn;
+  const uint32_t before = (uint32_t)((uint64_t)turn * dyTurns / turns);
+  if ((uint32_t)((uint64_t)(turn + 1) * dyTurns / turns) > before) {
+    spec_thread<T, Elt>(static_cast<const Elt*>(a.m2), a.out2, a.N, a.K2, a.Kpad2, a.kgCount,
+                        (size_t)(before * kSpec8Turn + blockIdx.x % kSpec8Turn) * 256 + threadIdx.x, a.tw);
+    return;
+  }
+  const size_t idx = (size_t)(blockIdx.x - before * kSpec8Turn) * 256 + threadIdx.x;
   if (idx >= (size_t)a.kgCount * 2 * a.Kpad) return;
   const int k = (int)(idx % a.Kpad);
   const size_t rest = idx / a.Kpad;
   const int half = (int)(rest & 1);
   const int kg = (int)(rest >> 1);
   const int row0 = kg * 2 * G + half * G;
-  const bool live = k < a.K;
-  const float gam = live && a.gamma ? (float)static_cast<const Elt*>(a.gamma)[k] : 1.0f;
-  const float bet = live && a.beta ? (float)static_cast<const Elt*>(a.beta)[k] : 0.0f;
+  const int rows = k < a.K ? min(G, a.N - row0) : 0;  // rows of this thread that exist
+  constexpr int WORDS = (T + 3) / 4;
   // A channel's T features lie in one block of 32 where T divides 32, else in at most two.
   constexpr bool ONE = kCkptBlock % T == 0;
   const int b0 = k * T / kCkptBlock, b1 = (k * T + T - 1) / kCkptBlock;
-  const int cut = b1 * kCkptBlock - k * T;  // features from `cut` on take the second block's step
+  const int cut = b1 > b0 ? b1 * kCkptBlock - k * T : T;  // features from `cut` on take the second block's step
+  uint32_t w[G][WORDS], s0[G], s1[G];
+#pragma unroll
+  for (int e = 0; e < G; ++e) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[e][i] = 0;
+    s0[e] = s1[e] = 0;
+  }
+  float gam = 1.0f, bet = 0.0f;
+  if (rows > 0) {
+    const unsigned char* c = a.codes + (size_t)row0 * a.pitch + (size_t)k * T;
+    const unsigned char* sc = a.scales + (size_t)row0 * (a.pitch / kCkptBlock);
+    auto fetch = [&](int e) __attribute__((always_inline)) {
+      __builtin_memcpy(w[e], c + (size_t)e * a.pitch, T);
+      s0[e] = sc[(size_t)e * (a.pitch / kCkptBlock) + b0];
+      if (!ONE) s1[e] = sc[(size_t)e * (a.pitch / kCkptBlock) + b1];
+    };
+    if (rows >= G) {
+#pragma unroll
+      for (int e = 0; e < G; ++e) fetch(e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < G; ++e)
+        if (e < rows) fetch(e);
+    }
+    if constexpr (VIEW != kViewPlain) {
+      if (a.gamma) gam = (float)static_cast<const Elt*>(a.gamma)[k];
+      if (a.beta) bet = (float)static_cast<const Elt*>(a.beta)[k];
+    }
+  }
   float pl[T][G];
 #pragma unroll
   for (int e = 0; e < G; ++e) {
     float v[T], o[T];
-    const int row = row0 + e;
-    if (row < a.N && live) {
-      const unsigned char* c = a.codes + (size_t)row * a.pitch + (size_t)k * T;
-      const unsigned char* sc = a.scales + (size_t)row * (a.pitch / kCkptBlock);
-      const float s0 = scale_step(sc[b0]);
-      const float s1 = ONE ? s0 : scale_step(sc[b1]);
-      uint32_t w[(T + 3) / 4];
+    const float st0 = scale_step(s0[e]), st1 = ONE ? st0 : scale_step(s1[e]);
 #pragma unroll
-      for (int i = 0; i < (T + 3) / 4; ++i) w[i] = 0;
-      __builtin_memcpy(w, c, T);
-#pragma unroll
-      for (int h = 0; h < T; ++h) {
-        const float step = ONE ? s0 : (b1 > b0 && h >= cut ? s1 : s0);
-        const int code = (int)(int8_t)(w[h / 4] >> (8 * (h % 4)));
-        float q = (float)code * step;
-        q = __builtin_fmaf(q, gam, bet);
-        v[h] = a.act == 1 ? gelu_erf(q) : q;
+    for (int h = 0; h < T; ++h) {
+      const float q = (float)(int)(int8_t)(w[e][h / 4] >> (8 * (h % 4))) * (ONE || h < cut ? st0 : st1);
+      if constexpr (VIEW == kViewPlain) {
+        v[h] = q;
+      } else {
+        // Missing rows are zero before GELU, which keeps them so.
+        const float u = e < rows ? __builtin_fmaf(q, gam, bet) : 0.0f;
+        v[h] = VIEW == kViewGelu ? gelu_erf(u) : u;
       }
-    } else {
-#pragma unroll
-      for (int h = 0; h < T; ++h) v[h] = 0.0f;
     }
     Dft<T>::run(v, o, a.tw);
 #pragma unroll

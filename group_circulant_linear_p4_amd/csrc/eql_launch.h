@@ -41,6 +41,9 @@ hipError_t launch_bwdw_real_f16(int T, int DB, int CB, int WCN, const BwdwArgs& 
 hipError_t launch_bwdw_real_f32(int T, int DB, int CB, int WCN, const BwdwArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_bwdw_pair_f16(int T, int DB, int CB, int WCN, const BwdwArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_bwdw_pair_f32(int T, int DB, int CB, int WCN, const BwdwArgs& a, unsigned grid, hipStream_t s);
+// Both in one launch, on 64 x 64 tiles (DB = CB = 1, WCN = 2 on both sides; T >= 3).
+hipError_t launch_bwdw_both_f16(int T, const BwdwArgs& pair, const BwdwArgs& real, hipStream_t s);
+hipError_t launch_bwdw_both_f32(int T, const BwdwArgs& pair, const BwdwArgs& real, hipStream_t s);
 // Weight gradient with dy's transform fused into the GEMM (T in {1, 2, 4}).
 hipError_t launch_bwdw4(bool f16, int T, int NB, const Bwdw4Args& a, unsigned grid, hipStream_t s);
 // p4m: the tied C_4 weight from w, and the p4m weight gradient from the C_4 one.

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
         // Past the row's end h is zero, so the codes that pad the last block are too.
         const uint32_t sc = block_scale(top_bits(v[i]));
         if (live && f0 < a.pitch) {
-          store_codes8<STREAM>(a.codes + row * a.pitch + f0, encode8(v[i], sc));
+          *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(v[i], sc);
           if ((lane & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
         }
       }
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
     store_chunk8<Elt, false>(static_cast<Elt*>(a.y) + row * a.R + f0, n, o);
     if (a.codes) {
       const uint32_t sc = block_scale(top_bits(h));
-      store_codes8<false>(a.codes + row * a.pitch + f0, encode8(h, sc));
+      *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(h, sc);
       if ((threadIdx.x & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
     }
   }

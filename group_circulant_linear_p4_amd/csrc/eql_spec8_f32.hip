@@ -1,0 +1,12 @@
+// Instantiations of the half spectrum from an 8-bit checkpoint (fp32): every T and view.
+#include "eql_spec8_inst.h"
+
+namespace eql {
+
+hipError_t launch_spec8_f32(int T, int view, const Spec8Args& a, unsigned grid, hipStream_t s) {
+#define EQL_CASE(t) return spec8_view<t, float>(view, a, grid, s);
+  EQL_FOR_EACH_T(T, EQL_CASE)
+#undef EQL_CASE
+}
+
+}  // namespace eql
