@@ -11,7 +11,9 @@ weight-gradient workspace, holding x's half spectrum, alive until the backward. 
 layer over p4m's point group (rotations and reflections), run through the same kernels on
 the C_4 view described in include/eqlinear.h.  With a bias,
 GELU or a residual, the forward is eqlinear_fwd_fused (eqlinear_fwd_fused_train when the
-weight needs a gradient) and the backward starts with eqlinear_fused_epilogue_bwd.  Torch only allocates the buffers; every arithmetic step
+weight needs a gradient) and the backward starts with eqlinear_fused_epilogue_bwd.  EQLayerNorm is the
+equivariant layer norm, and EQMLPBlock the pre-norm MLP block built from both, which by default
+keeps its activations for the backward in 8 bits (include/eqlinear_block.h).  Torch only allocates the buffers; every arithmetic step
 runs in the HIP library.
 """
 from __future__ import annotations
@@ -21,9 +23,12 @@ import math
 import torch
 
 from . import (EQL_ACT_GELU, EQL_ACT_NONE, EQL_PACK_BWDX, EQL_PACK_FWD, eqlinear_bwd_w,
-               eqlinear_bwd_w_train, eqlinear_bwd_w_workspace_bytes, eqlinear_bwd_x,
-               eqlinear_bwd_x_train, eqlinear_fused_epilogue_bwd, eqlinear_fwd_fused_train, eqlinear_fwd_train,
-               eqlinear_fused_epilogue_bwd_workspace_bytes, eqlinear_fwd, eqlinear_fwd_fused,
+               eqlinear_bwd_w_ckpt8, eqlinear_bwd_w_train, eqlinear_bwd_w_workspace_bytes, eqlinear_bwd_x,
+               eqlinear_bwd_x_train, eqlinear_ckpt8_bytes, eqlinear_ckpt8_pack, eqlinear_ckpt8_spectrum,
+               eqlinear_fused_epilogue_bwd, eqlinear_fused_epilogue_bwd_ckpt8, eqlinear_fwd_fused_train,
+               eqlinear_fwd_train, eqlinear_fused_epilogue_bwd_workspace_bytes, eqlinear_fwd, eqlinear_fwd_fused,
+               eqlinear_layernorm_bwd, eqlinear_layernorm_bwd_ckpt8, eqlinear_layernorm_bwd_workspace_bytes,
+               eqlinear_layernorm_fwd,
                eqlinear_p4m_expand_weight, eqlinear_p4m_fold_weight_grad, eqlinear_pack_weight,
                eqlinear_packed_weight_bytes)
 
@@ -325,3 +330,194 @@ class EQLinearP4M(torch.nn.Module):
     def extra_repr(self) -> str:
         return "in_channels=%d, out_channels=%d, group=p4m" % (self.in_channels, self.out_channels)
 
+
+class EQLayerNormFunction(torch.autograd.Function):
+    """Layer norm of rows of C'*T features with one weight and bias per channel, shared by its
+    T group elements (include/eqlinear_block.h).  Kept for the backward: x and the rows'
+    statistics, or with ckpt8 the normalised rows in 8 bits and 1 / std."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, gamma, beta, T: int, eps: float, ckpt8: bool, grad_mode: bool):
+        R = x.shape[-1]
+        if T < 1 or R % T != 0:
+            raise ValueError("x has %d features, not a multiple of the group order %d" % (R, T))
+        Cp = R // T
+        for name, p in (("weight", gamma), ("bias", beta)):
+            if p is None:
+                continue
+            if p.dim() != 1 or p.numel() != Cp:
+                raise ValueError("%s must be 1-D with C' = %d values (one per channel, shared over the group), got "
+                                 "shape %s" % (name, Cp, tuple(p.shape)))
+            if p.dtype != x.dtype or p.device != x.device:
+                raise ValueError("x and %s must share a dtype (fp16 or fp32) and a device" % name)
+        x2 = x.reshape(-1, R).contiguous()
+        N = x2.shape[0]
+        gamma, beta = (None if p is None else p.contiguous() for p in (gamma, beta))
+        y = torch.empty_like(x2)
+        train = grad_mode and any(ctx.needs_input_grad[:3])
+        stat = lambda: torch.empty(N, dtype=torch.float32, device=x.device)  # noqa: E731
+        rstd = stat() if train else None
+        mean = stat() if train and not ckpt8 else None
+        ckpt = (torch.empty(eqlinear_ckpt8_bytes(N, Cp, T), dtype=torch.uint8, device=x.device)
+                if train and ckpt8 else None)
+        eqlinear_layernorm_fwd(x2, gamma, beta, y, ckpt, mean, rstd, N, Cp, T, eps, x.dtype)
+        ctx.save_for_backward(x2 if train and not ckpt8 else None, ckpt, mean, rstd, gamma)
+        ctx.sizes, ctx.dtype, ctx.has_beta = (N, Cp, T), x.dtype, beta is not None
+        return y.reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy: torch.Tensor):
+        x2, ckpt, mean, rstd, gamma = ctx.saved_tensors
+        N, Cp, T = ctx.sizes
+        dy2 = dy.reshape(N, Cp * T).to(ctx.dtype).contiguous()
+        dx = torch.empty_like(dy2)
+        param = lambda: torch.empty(Cp, dtype=ctx.dtype, device=dy2.device)  # noqa: E731
+        dg = param() if gamma is not None and ctx.needs_input_grad[1] else None
+        db = param() if ctx.has_beta and ctx.needs_input_grad[2] else None
+        ws_bytes = eqlinear_layernorm_bwd_workspace_bytes(N, Cp, T, ctx.dtype)
+        ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dy2.device)
+        if ckpt is None:
+            eqlinear_layernorm_bwd(dy2, x2, mean, rstd, gamma, None, dx, dg, db, ws, ws_bytes, N, Cp, T, ctx.dtype)
+        else:
+            eqlinear_layernorm_bwd_ckpt8(dy2, ckpt, rstd, gamma, None, dx, dg, db, ws, ws_bytes, N, Cp, T, ctx.dtype)
+        return dx.reshape(dy.shape) if ctx.needs_input_grad[0] else None, dg, db, None, None, None, None
+
+
+def eq_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                  group_order: int = 1, eps: float = 1e-5, ckpt8: bool = False) -> torch.Tensor:
+    """Layer norm over the last axis (C'*T features), weight and bias [C'].  ckpt8: keep the
+    normalised rows in 8 bits for the backward instead of x (a quarter or half of its memory;
+    the gradients are then those of the rounded rows)."""
+    return EQLayerNormFunction.apply(x, weight, bias, group_order, eps, ckpt8, torch.is_grad_enabled())
+
+
+class EQLayerNorm(torch.nn.Module):
+    """Equivariant layer norm over channels * T features: one weight and bias per channel."""
+
+    def __init__(self, channels: int, group_order: int = 4, eps: float = 1e-5, device=None, dtype=None,
+                 ckpt8: bool = False):
+        super().__init__()
+        self.channels, self.group_order, self.eps, self.ckpt8 = channels, group_order, eps, ckpt8
+        self.weight = torch.nn.Parameter(torch.ones(channels, device=device, dtype=dtype))
+        self.bias = torch.nn.Parameter(torch.zeros(channels, device=device, dtype=dtype))
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        return eq_layer_norm(x, self.weight, self.bias, self.group_order, self.eps, self.ckpt8)
+
+    def extra_repr(self) -> str:
+        return "channels=%d, group_order=%d, eps=%g, ckpt8=%s" % (self.channels, self.group_order, self.eps, self.ckpt8)
+
+
+class EQMLPBlock8bitFunction(torch.autograd.Function):
+    """y = x + W2 gelu(W1 norm(x) + b1) + b2 keeping, from the forward to the backward, the
+    normalised rows and GELU's input as 8-bit checkpoints and nothing else of their size.
+
+    Backward, second layer: its input is gelu of the kept values, so the checkpoint's spectrum
+    takes the place of the one eqlinear_fwd_train would have kept; then GELU's own backward;
+    first layer: its input is gamma h + beta; then the norm's, which adds the residual
+    branch's gradient dy."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, gamma, beta, w1, b1, w2, b2, eps: float, grad_mode: bool):
+        Hp, Cp, T = w1.shape
+        if w2.shape != (Cp, Hp, T):
+            raise ValueError("w2 must be [C', H', T] = %s for w1 [H', C', T], got %s" % ((Cp, Hp, T), tuple(w2.shape)))
+        if x.shape[-1] != Cp * T:
+            raise ValueError("x has %d features, the block expects C'*T = %d" % (x.shape[-1], Cp * T))
+        for name, p, n in (("norm weight", gamma, Cp), ("norm bias", beta, Cp), ("b1", b1, Hp), ("b2", b2, Cp)):
+            if p.dim() != 1 or p.numel() != n:
+                raise ValueError("%s must be 1-D with %d values, got shape %s" % (name, n, tuple(p.shape)))
+        if any(p.dtype != x.dtype or p.device != x.device for p in (gamma, beta, w1, b1, w2, b2)):
+            raise ValueError("x and the block's parameters must share a dtype (fp16 or fp32) and a device")
+        x2 = x.reshape(-1, Cp * T).contiguous()
+        gamma, beta, w1, b1, w2, b2 = (p.contiguous() for p in (gamma, beta, w1, b1, w2, b2))
+        N, dt, dev = x2.shape[0], x.dtype, x.device
+        train = grad_mode and any(ctx.needs_input_grad[:7])
+        bytes8 = lambda c: torch.empty(eqlinear_ckpt8_bytes(N, c, T), dtype=torch.uint8, device=dev)  # noqa: E731
+        h8 = bytes8(Cp) if train else None
+        pre8 = bytes8(Hp) if train else None
+        rstd = torch.empty(N, dtype=torch.float32, device=dev) if train else None
+        u, y = torch.empty_like(x2), torch.empty_like(x2)
+        a = torch.empty((N, Hp * T), dtype=dt, device=dev)
+        pre = torch.empty_like(a) if train else None
+        eqlinear_layernorm_fwd(x2, gamma, beta, u, h8, None, rstd, N, Cp, T, eps, dt)
+        eqlinear_fwd_fused(u, _packed(w1, EQL_PACK_FWD), b1, None, a, pre, N, Cp, Hp, T, dt, EQL_ACT_GELU)
+        if train:
+            eqlinear_ckpt8_pack(pre, pre8, N, Hp, T, dt)
+        eqlinear_fwd_fused(a, _packed(w2, EQL_PACK_FWD), b2, x2, y, None, N, Hp, Cp, T, dt, EQL_ACT_NONE)
+        ctx.save_for_backward(h8, rstd, pre8, gamma, beta, w1, w2)
+        ctx.rows = N
+        return y.reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy: torch.Tensor):
+        h8, rstd, pre8, gamma, beta, w1, w2 = ctx.saved_tensors
+        Hp, Cp, T = w1.shape
+        N, dt, dev = ctx.rows, w1.dtype, w1.device
+        need = ctx.needs_input_grad
+        empty = lambda *s: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+        scratch = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=dev)  # noqa: E731
+        dy2 = dy.reshape(N, Cp * T).to(dt).contiguous()
+
+        def layer(g, w, ckpt, scale, shift, act, out, inp, need_w, need_x):
+            """Input and weight gradient of one layer (inp -> out channels) for output gradient g."""
+            dx = empty(N, inp * T) if need_x else None
+            dw = torch.empty_like(w) if need_w else None
+            n = eqlinear_bwd_w_workspace_bytes(N, inp, out, T, dt)
+            if need_w and need_x:
+                ws = scratch(n)
+                eqlinear_ckpt8_spectrum(ckpt, scale, shift, act, ws, n, N, inp, out, T, dt)
+                eqlinear_bwd_x_train(g, _packed(w, EQL_PACK_BWDX), dx, ws, n, N, inp, out, T, dt)
+                eqlinear_bwd_w_train(g, dw, ws, n, N, inp, out, T, dt)
+            elif need_x:
+                eqlinear_bwd_x(g, _packed(w, EQL_PACK_BWDX), dx, N, inp, out, T, dt)
+            elif need_w:
+                eqlinear_bwd_w_ckpt8(ckpt, scale, shift, act, g, dw, scratch(n), n, N, inp, out, T, dt)
+            return dx, dw
+
+        db2 = empty(Cp) if need[6] else None
+        if db2 is not None:
+            n = eqlinear_fused_epilogue_bwd_workspace_bytes(N, Cp, T, dt)
+            eqlinear_fused_epilogue_bwd(dy2, None, dy2, db2, scratch(n), n, N, Cp, T, dt, EQL_ACT_NONE)
+        below1, below = any(need[:4]), any(need[:3])  # gradients under the first layer's output, and under its input
+        dh, dw2 = layer(dy2, w2, pre8, None, None, EQL_ACT_GELU, Cp, Hp, need[5], below1 or need[4])
+        db1 = empty(Hp) if need[4] else None
+        dw1 = dx = dgamma = dbeta = None
+        if dh is not None:
+            n = eqlinear_fused_epilogue_bwd_workspace_bytes(N, Hp, T, dt)
+            eqlinear_fused_epilogue_bwd_ckpt8(dh, pre8, dh, db1, scratch(n), n, N, Hp, T, dt)
+            du, dw1 = layer(dh, w1, h8, gamma, beta, EQL_ACT_NONE, Hp, Cp, need[3], below)
+            if below:
+                dgamma, dbeta = (empty(Cp) if k else None for k in need[1:3])
+                n = eqlinear_layernorm_bwd_workspace_bytes(N, Cp, T, dt)
+                eqlinear_layernorm_bwd_ckpt8(du, h8, rstd, gamma, dy2, du, dgamma, dbeta, scratch(n), n, N, Cp, T, dt)
+                dx = du.reshape(dy.shape) if need[0] else None
+        return dx, dgamma, dbeta, dw1, db1, dw2, db2, None, None
+
+
+class EQMLPBlock(torch.nn.Module):
+    """Pre-norm transformer MLP block, x + W2 gelu(W1 norm(x) + b1) + b2, over C_T: channels*T ->
+    hidden_channels*T -> channels*T features.
+
+    ckpt8 (the default) keeps the normalised rows and GELU's input in 8 bits for the backward:
+    about C' + H' bytes per group element and row, against 2 C' + 4 H' in fp16 (4 C' + 8 H' in
+    fp32) and as much again for the kept spectra when it is off; the gradients are those of the
+    rounded activations (each within 1/127 of its block's largest)."""
+
+    def __init__(self, channels: int, hidden_channels: int, group_order: int = 4, eps: float = 1e-5, device=None,
+                 dtype=None, ckpt8: bool = True):
+        super().__init__()
+        self.ckpt8 = ckpt8
+        self.norm = EQLayerNorm(channels, group_order, eps, device=device, dtype=dtype)
+        self.fc1 = EQLinear(channels, hidden_channels, group_order, bias=True, activation="gelu", device=device, dtype=dtype)
+        self.fc2 = EQLinear(hidden_channels, channels, group_order, bias=True, device=device, dtype=dtype)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        n, a, b = self.norm, self.fc1, self.fc2
+        if self.ckpt8:
+            return EQMLPBlock8bitFunction.apply(x, n.weight, n.bias, a.weight, a.bias, b.weight, b.bias, n.eps,
+                                                torch.is_grad_enabled())
+        return b(a(n(x)), residual=x)
+
+    def extra_repr(self) -> str:
+        return "ckpt8=%s" % self.ckpt8

@@ -92,3 +92,21 @@ def bwd_w(v, dy, T):
     for t in range(T):
         out[:, :, t] = sum(dense[:, g, :, (g - t) % T] for g in range(T))
     return out
+
+
+def mlp_block(x, gamma, beta, w1, b1, w2, b2, eps, dy, ckpt8):
+    """(y, gradients by name) of x + W2 gelu(W1 norm(x) + b1) + b2 for output gradient dy; ckpt8: the
+    backward reads the normalised rows and GELU's input rounded to 8-bit checkpoints."""
+    import oracle
+    T = w1.shape[2]
+    u, h, _, rstd = norm(x, gamma, beta, T, eps)
+    pre = oracle.fwd(u, w1) + np.repeat(np.asarray(b1, np.float64), T)[None]
+    y = np.asarray(x, np.float64) + oracle.fwd(gelu(pre), w2) + np.repeat(np.asarray(b2, np.float64), T)[None]
+    if ckpt8:
+        h, pre = (unpack(*pack(v), v.shape[1]) for v in (h, pre))
+        u = affine(h, gamma, beta, T)
+    dy = np.asarray(dy, np.float64)
+    dpre, db1 = gelu_bwd(oracle.bwd_x(dy, w2), pre, T)
+    dx, dgamma, dbeta = norm_bwd(oracle.bwd_x(dpre, w1), h, rstd, gamma, T, dy)
+    return y, {"x": dx, "gamma": dgamma, "beta": dbeta, "w1": bwd_w(u, dpre, T), "b1": db1,
+               "w2": bwd_w(gelu(pre), dy, T), "b2": dy.reshape(dy.shape[0], -1, T).sum((0, 2))}

@@ -149,3 +149,39 @@ def test_binding_raises_and_refuses_host_tensors():
     assert e.value.status == eql.EQL_EALIGN and "eqlinear_ckpt8_pack" in str(e.value)
     with pytest.raises(ValueError):
         eql.eqlinear_layernorm_fwd(torch.zeros(8, 16), None, None, P[1], None, None, None, 8, 4, 4, 1e-5, F32, stream=0)
+
+
+@pytest.mark.parametrize("what", ["weight", "bias", "dtype", "features"])
+def test_layer_norm_layer_refuses(what):
+    """Refused before any buffer reaches the library (CPU tensors: nothing is launched)."""
+    import torch
+    from group_circulant_linear_p4_amd.layer import eq_layer_norm
+    x, g, b, t = torch.zeros(5, 12), torch.ones(3), torch.zeros(3), 4
+    if what == "weight":
+        g = torch.ones(12)
+    elif what == "bias":
+        b = torch.zeros(1, 3)
+    elif what == "dtype":
+        g = g.half()
+    else:
+        t = 5
+    with pytest.raises(ValueError, match="features" if what == "features" else "weight" if what != "bias" else "bias"):
+        eq_layer_norm(x, g, b, t)
+
+
+@pytest.mark.parametrize("what", ["w2", "x", "b1", "dtype"])
+def test_mlp_block_refuses(what):
+    import torch
+    from group_circulant_linear_p4_amd.layer import EQMLPBlock
+    block = EQMLPBlock(3, 5, 4)
+    x = torch.zeros(2, 12)
+    if what == "w2":
+        block.fc2.weight = torch.nn.Parameter(torch.zeros(3, 4, 4))
+    elif what == "x":
+        x = torch.zeros(2, 16)
+    elif what == "b1":
+        block.fc1.bias = torch.nn.Parameter(torch.zeros(20))
+    else:
+        x = x.half()
+    with pytest.raises(ValueError, match={"w2": "w2", "x": "features", "b1": "b1", "dtype": "dtype"}[what]):
+        block(x)
