@@ -23,6 +23,9 @@ int status_of(hipError_t e) { return e == hipSuccess ? EQL_OK : EQL_EHIP; }
 // caches; smaller ones often find them there.
 bool streams(int64_t bytes) { return bytes > (256LL << 20); }
 
+// Workgroups of 1024 threads that the GELU backward aims at.
+constexpr int64_t kEpi8Workgroups = 256;
+
 // Workgroups for `turns` turns of a grid-stride loop: at most `most`, all with the same number
 // of turns or one less.
 int64_t even_grid(int64_t turns, int64_t most) { return ceil_div(turns, ceil_div(turns, most)); }
@@ -253,12 +256,18 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   a.codes = static_cast<const unsigned char*>(pre_ckpt);
   a.scales = a.codes ? a.codes + N * a.pitch : nullptr;
   a.part = parts ? static_cast<float*>(workspace) : nullptr;
-  // Chunks across a workgroup: the row's chunks spread evenly over as few column blocks as hold
-  // them; a narrow row leaves room for more rows at a time.
+  // Chunks across a workgroup: the row's chunks spread evenly over column blocks, which leaves room
+  // for 1024 / lanes rows at a time.  As few column blocks as hold the row, or more (down to 32
+  // lanes) until there is a workgroup per compute unit; then row blocks as tall as keep it so,
+  // each leaving one sum a feature to add (and no more of them than the workspace is sized for).
   const int64_t chunks = ceil_div(a.R, 8);
-  a.colBlocks = (int)ceil_div(chunks, kEpi8Threads);
-  a.lanes = (int)ceil_div(chunks, a.colBlocks);
-  a.groups = kEpi8Threads / a.lanes;
+  int64_t colBlocks = ceil_div(chunks, kEpi8Threads);
+  while (rowBlocks * colBlocks < kEpi8Workgroups && ceil_div(chunks, 2 * colBlocks) >= 32) colBlocks *= 2;
+  a.lanes = (int)ceil_div(chunks, colBlocks);
+  a.colBlocks = (int)ceil_div(chunks, a.lanes);
+  rowsPerBlock = std::max(rowsPerBlock, ceil_div(N, std::max<int64_t>(1, kEpi8Workgroups / a.colBlocks)));
+  rowBlocks = ceil_div(N, rowsPerBlock);
+  a.groups = (int)std::min<int64_t>(kEpi8Threads / a.lanes, rowsPerBlock);
   a.rowsPerBlock = (int)rowsPerBlock;
   if (rowBlocks * a.colBlocks > kMaxGrid / 4) return EQL_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -47,38 +47,59 @@ __device__ __forceinline__ typename Chunk<Elt>::V zero_chunk() {
 }
 
 // The chunk at p, of which `n` elements exist (the others are zero).  WHOLE: every chunk is
-// whole or missing (R a multiple of 8), so no element-wise tail is compiled.  STREAM: a
-// non-temporal load, for operands that the caches cannot hold anyway.
+// whole or missing (R a multiple of 8), so no tail is compiled and rows are 16-byte aligned.
+// STREAM: a non-temporal load, for operands that the caches cannot hold anyway; never of rows
+// that start inside a line, whose lines two loads share.
 template <typename Elt, bool WHOLE, bool STREAM>
 __device__ __forceinline__ typename Chunk<Elt>::V load_chunk8(const Elt* p, int n) {
   typename Chunk<Elt>::V v = zero_chunk<Elt>();
   if (n >= 8) {
     const auto* q = reinterpret_cast<const typename Chunk<Elt>::VU*>(p);
-    if constexpr (STREAM) v = __builtin_nontemporal_load(q);
+    if constexpr (WHOLE && STREAM) v = __builtin_nontemporal_load(q);
     else v = *q;
   } else if (!WHOLE && n > 0) {
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < n) v[e] = p[e];
+    // The row's last 1 to 7 elements as 4 + 2 + 1.
+    typedef Elt E4 __attribute__((ext_vector_type(4), aligned(sizeof(Elt))));
+    typedef Elt E2 __attribute__((ext_vector_type(2), aligned(sizeof(Elt))));
+    E4 a = (E4)(Elt)0;
+    E2 b = (E2)(Elt)0;
+    Elt c = (Elt)0;
+    if (n & 4) a = *reinterpret_cast<const E4*>(p);
+    if (n & 2) b = *reinterpret_cast<const E2*>(p + (n & 4));
+    if (n & 1) c = p[n & 6];
+    const bool four = n & 4, two = n & 2;
+    const Elt z = (Elt)0, r0 = two ? b[0] : c, r1 = two ? b[1] : z, r2 = two ? c : z;
+    v[0] = four ? a[0] : r0;
+    v[1] = four ? a[1] : r1;
+    v[2] = four ? a[2] : r2;
+    v[3] = four ? a[3] : z;
+    v[4] = four ? r0 : z;
+    v[5] = four ? r1 : z;
+    v[6] = four ? r2 : z;
   }
   return v;
 }
 
 // Results are written past the caches, 16 bytes a lane: nothing in the same kernel reads them
-// again.  (Codes, 8 bytes a lane, are not: as non-temporal stores they took the norm's forward
-// pass with its checkpoint at N = 65536, R = 4096 from 228 to 273 us, and a small step soon
-// reads them again.)
+// again (also where rows start inside a line: N = 19019, R = 1452 fp16, the norm's forward pass
+// 30 us and 40 through the caches).  Codes, 8 bytes a lane, are not: as non-temporal stores they
+// took that pass with its checkpoint at N = 65536, R = 4096 from 228 to 273 us.
 template <typename Elt, bool WHOLE>
 __device__ __forceinline__ void store_chunk8(Elt* p, int n, const float (&f)[8]) {
-  if (n >= 8) {
-    typename Chunk<Elt>::VU v;
+  typename Chunk<Elt>::VU v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (Elt)f[e];
+  for (int e = 0; e < 8; ++e) v[e] = (Elt)f[e];
+  if (n >= 8) {
     __builtin_nontemporal_store(v, reinterpret_cast<typename Chunk<Elt>::VU*>(p));
   } else if (!WHOLE && n > 0) {
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < n) p[e] = (Elt)f[e];
+    // As 4 + 2 + 1.
+    typedef Elt E4 __attribute__((ext_vector_type(4), aligned(sizeof(Elt))));
+    typedef Elt E2 __attribute__((ext_vector_type(2), aligned(sizeof(Elt))));
+    const bool four = n & 4;
+    const Elt g0 = four ? v[4] : v[0], g1 = four ? v[5] : v[1], g2 = four ? v[6] : v[2];
+    if (four) *reinterpret_cast<E4*>(p) = (E4){v[0], v[1], v[2], v[3]};
+    if (n & 2) *reinterpret_cast<E2*>(p + (n & 4)) = (E2){g0, g1};
+    if (n & 1) p[n & 6] = n & 2 ? g2 : g0;
   }
 }
 

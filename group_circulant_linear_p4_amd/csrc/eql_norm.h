@@ -95,8 +95,10 @@ __device__ __forceinline__ typename Chunk<Elt>::V spread(const void* p, int f0, 
   if (!p || f0 >= R) return v;
   const Elt* q = static_cast<const Elt*>(p);
   const bool whole = f0 + 8 <= R;
-  if (T == 4 && whole) {
-    const E2 u = *reinterpret_cast<const E2*>(q + f0 / 4);
+  if (T == 4) {
+    const int c = f0 / 4;
+    E2 u = (E2)q[c];
+    if (whole) u = *reinterpret_cast<const E2*>(q + c);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = u[e / 4];
   } else if ((T & 7) == 0) {
@@ -104,10 +106,11 @@ __device__ __forceinline__ typename Chunk<Elt>::V spread(const void* p, int f0, 
   } else if (T == 1 && whole) {
     v = *reinterpret_cast<const typename Chunk<Elt>::VU*>(q + f0);
   } else {
+    const int last = R / T - 1;  // features past the row's end take the last channel's (unused)
     int c = f0 / T, t = f0 - c * T;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (f0 + e < R) v[e] = q[c];
+      v[e] = q[min(c, last)];
       if (++t == T) {
         t = 0;
         ++c;
@@ -160,7 +163,10 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
     float q[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const int n = a.R - (lane + i * LPR) * 8;
+      int n = a.R - (lane + i * LPR) * 8;
+      // Compared afresh in every turn: kept over the loop, the 8 K lane masks of the last chunk's
+      // elements would spill the scalar registers.
+      if constexpr (!WHOLE) asm volatile("" : "+v"(n));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[i][e] = (WHOLE ? n >= 8 : e < n) ? v[i][e] - mean : 0.0f;
