@@ -123,22 +123,34 @@ __device__ __forceinline__ float dpp_add(float v) {
   return v + __builtin_bit_cast(float, dpp_move<CTRL>(__builtin_bit_cast(uint32_t, v)));
 }
 
-// Scale byte of the block this lane's quad holds, from the lane's largest |v| (as bits: an
-// infinity or a NaN compares above every finite magnitude).  The exponent of 127.5 2^e is
-// e + 6 and its mantissa field 0x7F0000, so adding 0x10000 to the magnitude's bits carries
-// into the exponent exactly from 127.5 2^e on.
-__device__ __forceinline__ uint32_t block_scale(uint32_t top) {
-  top = max(top, dpp_move<kDppXor1>(top));
-  top = max(top, dpp_move<kDppXor2>(top));
-  const int s = (int)((top + 0x10000u) >> 23) - 6;
-  return top >= 0x7F800000u ? 255u : (uint32_t)max(s, 1);
+// Largest |v| of a chunk, and over the quad of lanes that holds a block.  NaN loses against a
+// number here; whether a block is finite is asked separately.
+__device__ __forceinline__ float chunk_top(const float (&v)[8]) {
+  float t = __builtin_fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1]));
+#pragma unroll
+  for (int e = 2; e < 8; ++e) t = __builtin_fmaxf(t, __builtin_fabsf(v[e]));
+  return t;
+}
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, dpp_move<kDppXor1>(v));
+  return max(v, dpp_move<kDppXor2>(v));
 }
 
-// Codes of eight values under scale byte s, as two words.  v 2^-e + 1.5 2^23 in one fused
-// operation: the product is exact, the sum rounds to the integer (ties to even), and the
-// integer is in the low bits of the result.
-__device__ __forceinline__ u32x2 encode8(const float (&v)[8], uint32_t s) {
-  const float back = s == 255u ? 0.0f : __builtin_bit_cast(float, (254u - s) << 23);
+// A block's step from its largest magnitude (a finite float's bits): e + 127 as the exponent field
+// of `top` less 6.  127.5 2^e has exponent e + 6 and mantissa field 0x7F0000, so adding 0x10000
+// carries into the exponent exactly from there on; e is at least -126.
+struct BlockStep {
+  float back;      // 2^-e
+  uint32_t scale;  // e + 127
+};
+__device__ __forceinline__ BlockStep block_step(uint32_t top) {
+  const uint32_t t = max((top + 0x10000u) & 0x7F800000u, 7u << 23);
+  return {__builtin_bit_cast(float, 0x82000000u - t), (t >> 23) - 6u};
+}
+
+// Codes of eight values, as two words.  v 2^-e + 1.5 2^23 in one fused operation: the product is
+// exact, the sum rounds to the integer (ties to even), and the integer is in the low bits.
+__device__ __forceinline__ u32x2 encode8(const float (&v)[8], float back) {
   uint32_t w[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = __builtin_bit_cast(uint32_t, __builtin_fmaf(v[e], back, 12582912.0f));
@@ -150,13 +162,6 @@ __device__ __forceinline__ u32x2 encode8(const float (&v)[8], uint32_t s) {
     r[h] = lo | hi;
   }
   return r;
-}
-
-__device__ __forceinline__ uint32_t top_bits(const float (&v)[8]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu);
-  return top;
 }
 
 // The step 2^e of a scale byte (NaN for 255).
@@ -206,9 +211,14 @@ __global__ void __launch_bounds__(256) eql_ckpt_pack_kernel(const CkptArgs a) {
   float f[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
-  const uint32_t s = block_scale(top_bits(f));
-  *reinterpret_cast<u32x2*>(a.codes + idx * 8) = encode8(f, s);
-  if ((threadIdx.x & 3) == 0) a.scales[idx >> 2] = (unsigned char)s;
+  // As bits, an infinity or a NaN compares above every finite magnitude.
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu);
+  top = quad_max(top);
+  const BlockStep st = block_step(top);
+  *reinterpret_cast<u32x2*>(a.codes + idx * 8) = encode8(f, st.back);
+  if ((threadIdx.x & 3) == 0) a.scales[idx >> 2] = (unsigned char)(top >= 0x7F800000u ? 255u : st.scale);
 }
 
 template <typename Elt, bool WHOLE, bool STREAM>

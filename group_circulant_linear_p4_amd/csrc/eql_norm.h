@@ -35,10 +35,14 @@ struct NormArgs {
   const void* dy;     // backward: [N][R]
   const void* dres;   // [N][R] or null
   void* dx;           // [N][R] (may be dy or dres)
+  void* dgamma;       // backward by one workgroup: [C], written by it (then part is null)
+  void* dbeta;
   float* part;        // [gridDim][2][C] column sums (wide: [rowBlocks][2][R]), or null
   float* rowSums;     // wide backward: [N][2], mean(g) and mean(g h)
   int64_t N;
   int R, C, T, pitch;
+  uint32_t perT;      // ceil(2^32 / T) for T > 1: f / T is the product's high word (f < 2^28)
+  int table;          // 1: parameters spread through LDS (norm_table)
   float eps, invR;
   int rowsPerBlock, colBlocks;  // wide backward
 };
@@ -85,45 +89,92 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
   }
 }
 
-// One per-channel parameter spread over the 8 features of a chunk (as elements).  Common group
-// orders fetch their 8 / T channels at once (for T = 4: one 4-byte load of fp16 where eight
-// would do, 48 loads a lane less at R = 384); T = 8 and 16 have one channel a chunk.
+__device__ __forceinline__ int channel_of(const NormArgs& a, int f) {
+  return a.T == 1 ? f : (int)__umulhi((uint32_t)f, a.perT);
+}
+
+// One per-channel parameter spread over the 8 features of a chunk (as elements; features past the
+// row's end take any channel's).  The chunk's channels are fetched once each: 8 / T in one load
+// where T is 1, 2 or 4, one where 8 divides T, else the four that it can touch at most.
 template <typename Elt>
-__device__ __forceinline__ typename Chunk<Elt>::V spread(const void* p, int f0, int R, int T, float missing) {
+__device__ __forceinline__ typename Chunk<Elt>::V spread(const NormArgs& a, const void* p, int f0, float missing) {
   typedef Elt E2 __attribute__((ext_vector_type(2), aligned(sizeof(Elt))));
+  typedef Elt E4 __attribute__((ext_vector_type(4), aligned(sizeof(Elt))));
+  const int R = a.R, T = a.T;
   typename Chunk<Elt>::V v = (typename Chunk<Elt>::V)(Elt)missing;
   if (!p || f0 >= R) return v;
   const Elt* q = static_cast<const Elt*>(p);
   const bool whole = f0 + 8 <= R;
   if (T == 4) {
-    const int c = f0 / 4;
-    E2 u = (E2)q[c];
-    if (whole) u = *reinterpret_cast<const E2*>(q + c);
+    E2 u = (E2)q[f0 / 4];  // a partial chunk is one channel
+    if (whole) u = *reinterpret_cast<const E2*>(q + f0 / 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = u[e / 4];
-  } else if ((T & 7) == 0) {
-    v = (typename Chunk<Elt>::V)q[f0 / T];
+  } else if (T == 2 && whole) {
+    const E4 u = *reinterpret_cast<const E4*>(q + f0 / 2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = u[e / 2];
   } else if (T == 1 && whole) {
     v = *reinterpret_cast<const typename Chunk<Elt>::VU*>(q + f0);
+  } else if ((T & 7) == 0) {
+    v = (typename Chunk<Elt>::V)q[channel_of(a, f0)];
+  } else if (T == 1) {  // the row's last, partial chunk
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (f0 + e < R) v[e] = q[f0 + e];
   } else {
-    const int last = R / T - 1;  // features past the row's end take the last channel's (unused)
-    int c = f0 / T, t = f0 - c * T;
+    const int last = a.C - 1, c = channel_of(a, f0), t = f0 - c * T;
+    const Elt u0 = q[c], u1 = q[min(c + 1, last)], u2 = q[min(c + 2, last)], u3 = q[min(c + 3, last)];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[e] = q[min(c, last)];
-      if (++t == T) {
-        t = 0;
-        ++c;
-      }
+      const int x = t + e;  // at most T + 6, below 4 T
+      v[e] = x >= 2 * T ? (x >= 3 * T ? u3 : u2) : (x >= T ? u1 : u0);
     }
   }
   return v;
+}
+
+// The other group orders' parameters go through a table of the row's features in LDS, filled by
+// the whole workgroup: selecting among four channels for every chunk is some 100 operations, and
+// in a small launch, one wave to a SIMD, they took longer than the rows (37 rows of R = 1752,
+// T = 12 fp16: 8.0 us forward and 5.1 with the table).  Not where a row takes the whole workgroup:
+// each entry would serve one lane once (199 rows of R = 4542, T = 6: 8.2 us and 10.4 with it).
+// Features to the end of the last chunk are defined.
+constexpr int64_t kNormTableBytes = 32768;
+__host__ __device__ constexpr int norm_table_row(int R) { return (R + 7) / 8 * 8; }
+__host__ constexpr bool norm_table(int lpr, int R, int T, int elt, int params) {
+  return lpr < 256 && T != 1 && T != 2 && T != 4 && T != 8 && T != 16 && (int64_t)norm_table_row(R) * elt * params <= kNormTableBytes;
+}
+template <typename Elt>
+__device__ __forceinline__ void fill_table(const NormArgs& a, Elt* table, const void* p, float missing) {
+  const Elt* q = static_cast<const Elt*>(p);
+#pragma unroll 4
+  for (int f = (int)threadIdx.x; f < norm_table_row(a.R); f += 256) {
+    const int c = min(channel_of(a, f), a.C - 1);
+    table[f] = q ? q[c] : (Elt)missing;
+  }
+}
+
+// 1 / sqrt(a) from the hardware's approximation and one Newton step, within an ulp or so.  NaN for
+// a = 0 and a = infinity: a constant row without eps, and one whose squares overflow.
+__device__ __forceinline__ float inv_sqrt(float a) {
+  const float r = __builtin_amdgcn_rsqf(a);
+  return __builtin_fmaf(0.5f * r, __builtin_fmaf(-a * r, r, 1.0f), r);
+}
+
+// A checkpoint block of normalised rows: h is NaN throughout exactly when rstd is.
+__device__ __forceinline__ void store_block(const NormArgs& a, int64_t row, int f0, const float (&h)[8], float back,
+                                            uint32_t scale, float rstd, bool scaleLane) {
+  *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(h, back);
+  if (scaleLane)
+    a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)(__builtin_isnan(rstd) ? 255u : scale);
 }
 
 template <typename Elt, int LPR, int K, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
   using V = typename Chunk<Elt>::V;
   constexpr int G = 256 / LPR;
+  extern __shared__ __align__(16) float lds[];  // the parameters' table, if there is one
   __shared__ float red[2][8];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
   const int64_t step = (int64_t)gridDim.x * G;
@@ -139,11 +190,24 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
   };
   load((int64_t)blockIdx.x * G + grp);
   V gam[K], bet[K];
+  if (a.table) {
+    Elt* table = reinterpret_cast<Elt*>(lds);
+    const int size = norm_table_row(a.R);
+    fill_table(a, table, a.gamma, 1.0f);
+    fill_table(a, table + size, a.beta, 0.0f);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int f0 = (lane + i * LPR) * 8;
-    gam[i] = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
-    bet[i] = spread<Elt>(a.beta, f0, a.R, a.T, 0.0f);
+    for (int i = 0; i < K; ++i) {
+      const int f0 = min((lane + i * LPR) * 8, size - 8);
+      gam[i] = *reinterpret_cast<const V*>(table + f0);
+      bet[i] = *reinterpret_cast<const V*>(table + size + f0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      gam[i] = spread<Elt>(a, a.gamma, (lane + i * LPR) * 8, 1.0f);
+      bet[i] = spread<Elt>(a, a.beta, (lane + i * LPR) * 8, 0.0f);
+    }
   }
   for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += step) {
     const int64_t row = base + grp;
@@ -163,19 +227,23 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
     float q[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      int n = a.R - (lane + i * LPR) * 8;
-      // Compared afresh in every turn: kept over the loop, the 8 K lane masks of the last chunk's
-      // elements would spill the scalar registers.
-      if constexpr (!WHOLE) asm volatile("" : "+v"(n));
+      float t = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] = (WHOLE ? n >= 8 : e < n) ? v[i][e] - mean : 0.0f;
-        q[0] = __builtin_fmaf(v[i][e], v[i][e], q[0]);
+      for (int e = 0; e < 8; ++e) v[i][e] -= mean;
+      int n = a.R - (lane + i * LPR) * 8;
+      if (!WHOLE && a.R < (i + 1) * LPR * 8) {
+        // The row ends among these chunks: its missing features count as zero.  (Compared afresh
+        // in every turn: kept over the loop, the lane masks would spill the scalar registers.)
+        asm volatile("" : "+v"(n));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = e < n ? v[i][e] : 0.0f;
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t = __builtin_fmaf(v[i][e], v[i][e], t);
+      q[0] += WHOLE && n < 8 ? 0.0f : t;
     }
     row_sums<LPR>(q, red[1]);
-    // The square root and the quotient are correctly rounded.
-    const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(q[0], a.invR, a.eps));
+    const float rstd = inv_sqrt(__builtin_fmaf(q[0], a.invR, a.eps));
     if (live && lane == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -191,12 +259,11 @@ __global__ void __launch_bounds__(256) eql_norm_fwd_kernel(const NormArgs a) {
       }
       if (live) store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.y) + row * a.R + f0, a.R - f0, o);
       if (a.codes) {
-        // Past the row's end h is zero, so the codes that pad the last block are too.
-        const uint32_t sc = block_scale(top_bits(v[i]));
-        if (live && f0 < a.pitch) {
-          *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(v[i], sc);
-          if ((lane & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
-        }
+        // A missing chunk of the row's last block has codes zero (h is rstd times minus the mean).
+        const bool here = !WHOLE || f0 < a.R;
+        const uint32_t top = __builtin_bit_cast(uint32_t, chunk_top(v[i]));
+        const BlockStep st = block_step(quad_max(here ? top : 0u));
+        if (live && f0 < a.pitch) store_block(a, row, f0, v[i], here ? st.back : 0.0f, st.scale, rstd, (lane & 3) == 0);
       }
     }
   }
@@ -222,12 +289,12 @@ __device__ __forceinline__ float group_sum(float v) {
 __host__ __device__ constexpr int norm_bwd_copies(int lpr) { return lpr > 64 ? 1 : 4; }
 
 // CKPT: h from the checkpoint (codes, scales, rstd), else from x, mean and rstd.
-// Dynamic LDS: norm_bwd_copies(LPR) * R floats, for the column sums at the end.
+// Dynamic LDS: norm_bwd_copies(LPR) * R floats, for the column sums at the end, or the table.
 template <typename Elt, int LPR, int K, bool WHOLE, bool STREAM, bool CKPT>
 __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   using V = typename Chunk<Elt>::V;
   constexpr int G = 256 / LPR;
-  extern __shared__ float cols[];
+  extern __shared__ __align__(16) float lds[];  // the weight's table, then the column sums
   __shared__ float red[2][8];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
   const int64_t step = (int64_t)gridDim.x * G;
@@ -263,12 +330,21 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   load((int64_t)blockIdx.x * G + grp);
   V gam[K];
   float sg[K][8], sb[K][8];
+  if (a.table) {
+    Elt* table = reinterpret_cast<Elt*>(lds);
+    fill_table(a, table, a.gamma, 1.0f);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    gam[i] = spread<Elt>(a.gamma, (lane + i * LPR) * 8, a.R, a.T, 1.0f);
+    for (int i = 0; i < K; ++i)
+      gam[i] = *reinterpret_cast<const V*>(table + min((lane + i * LPR) * 8, norm_table_row(a.R) - 8));
+  } else {
+#pragma unroll
+    for (int i = 0; i < K; ++i) gam[i] = spread<Elt>(a, a.gamma, (lane + i * LPR) * 8, 1.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sg[i][e] = sb[i][e] = 0.0f;
-  }
   int turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += step) {
     const int64_t row = base + grp;
@@ -317,7 +393,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
       store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.dx) + row * a.R + f0, live ? a.R - f0 : 0, o);
     }
   }
-  if (!a.part) return;
+  if (!a.part && !a.dgamma && !a.dbeta) return;
   // Column sums: the row groups of a wave across its lanes, the waves through LDS, then per
   // channel its T features, in a fixed order.
   constexpr int COPIES = norm_bwd_copies(LPR);
@@ -326,6 +402,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.C;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
+    void* direct = which ? a.dbeta : a.dgamma;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < K; ++i) {
@@ -334,7 +411,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
       for (int e = 0; e < 8; ++e) {
         float t = which ? sb[i][e] : sg[i][e];
         if constexpr (LPR < 64) t = group_sum<LPR>(t);
-        if (writes && f0 + e < a.R) cols[copy * a.R + f0 + e] = t;
+        if (writes && f0 + e < a.R) lds[copy * a.R + f0 + e] = t;
       }
     }
     __syncthreads();
@@ -342,8 +419,9 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
       float t = 0.0f;
       for (int j = 0; j < a.T; ++j)
 #pragma unroll
-        for (int q = 0; q < COPIES; ++q) t += cols[q * a.R + c * a.T + j];
-      out[which * a.C + c] = t;
+        for (int q = 0; q < COPIES; ++q) t += lds[q * a.R + c * a.T + j];
+      if (a.part) out[which * a.C + c] = t;
+      else if (direct) static_cast<Elt*>(direct)[c] = (Elt)t;
     }
   }
 }
@@ -438,7 +516,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
     }
   }
   block_sums(q, red);
-  const float rstd = 1.0f / __builtin_sqrtf(__builtin_fmaf(q[0], a.invR, a.eps));
+  const float rstd = inv_sqrt(__builtin_fmaf(q[0], a.invR, a.eps));
   if (threadIdx.x == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
@@ -447,7 +525,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
   for (int f0 = (int)threadIdx.x * 8; f0 < a.pitch; f0 += 8192) {
     const int n = a.R - f0;
     const auto u = load_chunk8<Elt, false, false>(xr + f0, n);
-    const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f), bet = spread<Elt>(a.beta, f0, a.R, a.T, 0.0f);
+    const auto gam = spread<Elt>(a, a.gamma, f0, 1.0f), bet = spread<Elt>(a, a.beta, f0, 0.0f);
     float h[8], o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -456,9 +534,8 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
     }
     store_chunk8<Elt, false>(static_cast<Elt*>(a.y) + row * a.R + f0, n, o);
     if (a.codes) {
-      const uint32_t sc = block_scale(top_bits(h));
-      *reinterpret_cast<u32x2*>(a.codes + row * a.pitch + f0) = encode8(h, sc);
-      if ((threadIdx.x & 3) == 0) a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock] = (unsigned char)sc;
+      const BlockStep st = block_step(quad_max(__builtin_bit_cast(uint32_t, chunk_top(h))));
+      store_block(a, row, f0, h, st.back, st.scale, rstd, (threadIdx.x & 3) == 0);
     }
   }
 }
@@ -485,7 +562,7 @@ __global__ void __launch_bounds__(1024) eql_norm_bwd_rows_kernel(const NormArgs 
   for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
     const int n = a.R - f0;
     const auto d = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
-    const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+    const auto gam = spread<Elt>(a, a.gamma, f0, 1.0f);
     float h[8];
     wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
 #pragma unroll
@@ -506,7 +583,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_cols_kernel(const NormArgs a
   const int f0 = (cb * 256 + (int)threadIdx.x) * 8;
   const int n = a.R - f0;
   if (n <= 0) return;
-  const auto gam = spread<Elt>(a.gamma, f0, a.R, a.T, 1.0f);
+  const auto gam = spread<Elt>(a, a.gamma, f0, 1.0f);
   float sg[8], sb[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sg[e] = sb[e] = 0.0f;

@@ -32,7 +32,9 @@ hipError_t launch_norm_bwd(bool f16, bool stream, NormShape sh, bool ckpt, const
                        : (ckpt ? bwd_fn<float, true>(sh, whole, stream) : bwd_fn<float, false>(sh, whole, stream));
   if (!fn) return hipErrorInvalidValue;
   void* kargs[] = {const_cast<NormArgs*>(&a)};
-  const size_t lds = a.part ? (size_t)norm_bwd_copies(sh.lpr) * (size_t)a.R * sizeof(float) : 0;
+  const size_t sums = a.part || a.dgamma || a.dbeta ? (size_t)norm_bwd_copies(sh.lpr) * (size_t)a.R * sizeof(float) : 0;
+  const size_t table = a.table ? (size_t)norm_table_row(a.R) * (f16 ? 2 : 4) : 0;
+  const size_t lds = sums > table ? sums : table;
   return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, lds, s);
 }
 

@@ -31,7 +31,10 @@ static const void* fwd_fn(NormShape sh, bool whole, bool stream) {
 
 hipError_t launch_norm_fwd(bool f16, bool stream, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s) {
   const void* fn = f16 ? fwd_fn<_Float16>(sh, a.R % 8 == 0, stream) : fwd_fn<float>(sh, a.R % 8 == 0, stream);
-  return fn ? launch_kernel(fn, grid, a, s) : hipErrorInvalidValue;
+  if (!fn) return hipErrorInvalidValue;
+  void* kargs[] = {const_cast<NormArgs*>(&a)};
+  const size_t lds = a.table ? (size_t)norm_table_row(a.R) * (f16 ? 2 : 4) * 2 : 0;
+  return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, lds, s);
 }
 
 hipError_t launch_norm_fwd_wide(bool f16, const NormArgs& a, hipStream_t s) {
