@@ -297,26 +297,33 @@ constexpr int64_t kSmallPartialBytes = 1 << 20;
 // Row ranges of a reduction over kgCount k-steps for `tiles` output items whose
 // partials take partBytesPerSplit bytes per range: enough ranges to give every compute
 // unit one item.
-int64_t split_count(int64_t tiles, int64_t kgCount, int64_t partBytesPerSplit) {
+// balance (the gradient from a checkpoint; the others keep the ranges, and so the bits, that
+// they had): where that leaves too few ranges, as many as balance a range's serial chain, about
+// kStepSeconds a k-step, against writing and adding one more set of partials at kPartialRate:
+// chain / S + S partials is least at S = sqrt(chain / partials).
+constexpr double kStepSeconds = 1.3e-6, kPartialRate = 1.5e12;
+int64_t split_count(int64_t tiles, int64_t kgCount, int64_t partBytesPerSplit, bool balance) {
   const int64_t want = tiles >= kTargetWorkgroups ? 1 : kTargetWorkgroups / tiles;
   int64_t S = std::min<int64_t>(want, std::max<int64_t>(1, kgCount / kMinStepsPerSplit));
   if (S < want) {
     const int64_t S2 = std::min<int64_t>(want, std::max<int64_t>(1, kgCount / kMinStepsSmall));
     if (S2 * partBytesPerSplit <= kSmallPartialBytes) S = S2;
+    const double best = std::sqrt((double)kgCount * kStepSeconds * kPartialRate / (double)std::max<int64_t>(1, partBytesPerSplit));
+    if (balance) S = std::max(S, std::min(S2, (int64_t)best));
   }
   return S;
 }
 
 // Row ranges (k-step ranges) of one GEMM launch.
-void plan_splits(GemmPlan& g, int64_t kgCount, int64_t partBytesPerSplit) {
+void plan_splits(GemmPlan& g, int64_t kgCount, int64_t partBytesPerSplit, bool balance) {
   const int64_t tiles = g.groups * g.dTiles * g.cTiles;
   if (tiles == 0 || kgCount == 0) return;
-  const int64_t S = split_count(tiles, kgCount, partBytesPerSplit);
+  const int64_t S = split_count(tiles, kgCount, partBytesPerSplit, balance);
   g.kgPerSplit = ceil_div(kgCount, S);
   g.S = ceil_div(kgCount, g.kgPerSplit);
 }
 
-BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
+BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype, bool balance = false) {
   BwdwPlan p;
   const int nr = n_real_planes(T), np = n_pairs(T);
   const int64_t wd = tile_width(Dp), wc = tile_width(Cp);
@@ -365,7 +372,7 @@ BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
     p.fCTiles = ceil_div(Cp, 32 * p.fNB);
     p.Cpad = p.fCTiles * 32 * p.fNB;
     const int64_t tiles = p.fDTiles * p.fCTiles;
-    const int64_t S = split_count(tiles, p.kgCount, (int64_t)T * Dp * Cp * (int64_t)sizeof(float));
+    const int64_t S = split_count(tiles, p.kgCount, (int64_t)T * Dp * Cp * (int64_t)sizeof(float), balance);
     p.fKgPerSplit = ceil_div(p.kgCount, S);
     p.fS = ceil_div(p.kgCount, p.fKgPerSplit);
     p.real.S = p.pair.S = p.fS;
@@ -374,8 +381,8 @@ BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
     p.partPBytes = (size_t)p.fS * (T - nr) * (size_t)Dp * (size_t)Cp * sizeof(float);
     return p;
   }
-  plan_splits(p.real, p.kgCount, (int64_t)nr * Dp * Cp * (int64_t)sizeof(float));
-  plan_splits(p.pair, p.kgCount, (int64_t)(T - nr) * Dp * Cp * (int64_t)sizeof(float));
+  plan_splits(p.real, p.kgCount, (int64_t)nr * Dp * Cp * (int64_t)sizeof(float), balance);
+  plan_splits(p.pair, p.kgCount, (int64_t)(T - nr) * Dp * Cp * (int64_t)sizeof(float), balance);
   p.dyhBytes = align256((size_t)p.kgCount * T * 2 * (size_t)p.Dpad * 16);
   p.xhBytes = align256((size_t)p.kgCount * T * 2 * (size_t)p.Cpad * 16);
   p.partRBytes = align256((size_t)p.real.S * nr * (size_t)Dp * (size_t)Cp * sizeof(float));
@@ -559,7 +566,7 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
   int st = check_sizes(N, Cp, Dp, T, dtype);
   if (st != EQL_OK) return st;
   if (view && (st = check_view(*view, N, dtype)) != EQL_OK) return st;
-  const BwdwPlan p = plan_bwdw(N, Cp, Dp, T, dtype);
+  const BwdwPlan p = plan_bwdw(N, Cp, Dp, T, dtype, view != nullptr);
   const bool needX = !spectra && !view, needDy = !spectra || p.fused;
   if (!dw || (N > 0 && ((needX && !x) || (needDy && !dy) || !workspace))) return EQL_EINVAL;
   if (ws_bytes < p.total()) return EQL_EINVAL;
@@ -826,7 +833,7 @@ int eqlinear_bwd_x(const void* dy, const void* w_packed_bwdx, void* dx, int64_t 
 
 size_t eqlinear_bwd_w_workspace_bytes(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
   if (check_sizes(N, Cp, Dp, T, dtype) != EQL_OK) return 0;
-  return plan_bwdw(N, Cp, Dp, T, dtype).total();
+  return std::max(plan_bwdw(N, Cp, Dp, T, dtype).total(), plan_bwdw(N, Cp, Dp, T, dtype, true).total());
 }
 
 int eqlinear_bwd_w(const void* x, const void* dy, void* dw, void* workspace, size_t ws_bytes,
