@@ -23,7 +23,9 @@ int status_of(hipError_t e) { return e == hipSuccess ? EQL_OK : EQL_EHIP; }
 // caches; smaller ones often find them there.
 bool streams(int64_t bytes) { return bytes > (256LL << 20); }
 
-// Workgroups of 1024 threads that the GELU backward aims at.
+// Workgroups of 1024 threads that the GELU backward aims at: one per compute unit.  More do not
+// read faster (N = 12608, R = 1536 fp16: 20.4 us with 256, 20.3 with 512; N = 65536, R = 4096: 242 and
+// 252) and leave more partial sums (the bias kernel after them 5.6 and 7.8 us).
 constexpr int64_t kEpi8Workgroups = 256;
 
 // Workgroups for `turns` turns of a grid-stride loop: at most `most`, all with the same number

@@ -62,8 +62,8 @@ int eqlinear_ckpt8_unpack(const void* ckpt, void* x, int64_t N, int64_t Cp, int 
  *   (quantised from fp32).
  * mean, rstd: [N] floats, or NULL (4-byte aligned); the backward pass needs rstd, and mean
  *   unless it reads the checkpoint.
- * eps: >= 0 and finite, else EQL_EINVAL.  A row that holds an infinity or a NaN, or a constant
- *   row with eps = 0, gives NaN throughout.
+ * eps: >= 0 and finite, else EQL_EINVAL.  A row that holds an infinity or a NaN, or whose
+ *   squares overflow fp32, or a constant row with eps = 0, gives NaN throughout.
  * Rows over 16384 features take N <= 2^22 - 1 (EQL_EINVAL otherwise).
  */
 int eqlinear_layernorm_fwd(const void* x, const void* gamma, const void* beta, void* y, void* ckpt, float* mean,

@@ -30,7 +30,8 @@ F32ERR = 1e-5
 # 8 or 32 divides; rows past what the registers hold, backward (8192) and forward (16384).
 SHAPES = [(1, 1, 1), (1, 5, 3), (3, 8, 4), (197, 96, 4), (33, 171, 3), (64, 133, 5), (17, 64, 8), (2500, 16, 1),
           (1100, 3, 16), (300, 7, 1), (129, 129, 4), (70, 512, 4), (41, 513, 4), (9, 1024, 4), (6, 1500, 4), (5, 2048, 4),
-          (3, 2731, 3), (700, 8200, 1), (2, 4099, 4), (1, 20011, 1)]
+          (3, 2731, 3), (700, 8200, 1), (2, 4099, 4), (1, 20011, 1), (12, 96, 4), (50, 99, 2), (21, 66, 9), (13, 400, 12),
+          (4, 700, 12), (11, 300, 15), (515, 31, 7)]
 
 
 def dev(a):
@@ -283,7 +284,8 @@ def test_non_finite_rows_stay_in_their_rows():
         assert torch.isnan(dg).all().item() and torch.isfinite(db).all().item()
 
 
-GELU_SHAPES = [(1, 1, 1), (3, 8, 4), (197, 384, 4), (501, 171, 3), (64, 133, 5), (2500, 16, 1), (30, 700, 3), (9, 2051, 4)]
+GELU_SHAPES = [(1, 1, 1), (3, 8, 4), (197, 384, 4), (501, 171, 3), (64, 133, 5), (2500, 16, 1), (30, 700, 3), (9, 2051, 4),
+               (3001, 40, 4), (700, 300, 7), (20, 900, 16)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
