@@ -123,18 +123,22 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(buf):
+    # The usual case first: small calls are bound by their host time.
     if buf is None:
         return None
+    if type(buf) is not int:
+        try:
+            if buf.is_cuda and buf.is_contiguous():
+                return buf.data_ptr() or None
+        except AttributeError:
+            pass
     if isinstance(buf, int):
         return buf or None
-    data_ptr = getattr(buf, "data_ptr", None)
-    if data_ptr is None:
+    if getattr(buf, "data_ptr", None) is None:
         raise TypeError("expected a device tensor or an int address, got %r" % type(buf))
     if not buf.is_cuda:
         raise ValueError("EQ-Linear buffers must live in GPU memory (got a %s tensor)" % buf.device)
-    if not buf.is_contiguous():
-        raise ValueError("EQ-Linear buffers must be contiguous")
-    return data_ptr() or None
+    raise ValueError("EQ-Linear buffers must be contiguous")
 
 
 _raw_stream = None
@@ -161,14 +165,19 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream) or None
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype(dtype) -> int:
+    code = _dtype_codes.get(dtype)
+    if code is not None:
+        return code
     if isinstance(dtype, int):
         return dtype
     import torch
-    if dtype == torch.float16:
-        return EQL_F16
-    if dtype == torch.float32:
-        return EQL_F32
+    _dtype_codes.update({torch.float16: EQL_F16, torch.float32: EQL_F32})
+    if dtype in _dtype_codes:
+        return _dtype_codes[dtype]
     raise ValueError("unsupported dtype %r (fp16 or fp32)" % (dtype,))
 
 
