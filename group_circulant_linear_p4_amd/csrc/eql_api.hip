@@ -531,9 +531,9 @@ int check_view(const host::CkptView& v, int64_t N, int dtype) {
 // dy also dy's (K2 channels) in the same launch.
 int run_spec8(const host::CkptView& v, void* out, int64_t N, int64_t K, int64_t Kpad, int64_t kgCount, int T, int dtype,
               hipStream_t s, const void* dy = nullptr, void* outDy = nullptr, int64_t K2 = 0, int64_t Kpad2 = 0) {
-  const auto grid_of = [&](int64_t pad) { return ceil_div(kgCount * 2 * pad, 256 * kSpec8Turn) * kSpec8Turn; };
-  const int64_t grid2 = dy ? grid_of(Kpad2) : 0;
-  const int64_t grid = grid2 + grid_of(Kpad);
+  const auto grid_of = [&](int64_t ch) { return ceil_div(kgCount * 2 * ch, 256 * kSpec8Turn) * kSpec8Turn; };
+  const int64_t grid2 = dy ? grid_of(K2) : 0;
+  const int64_t grid = grid2 + grid_of(K);
   if (grid > kMaxGrid) return EQL_EINVAL;
   Spec8Args a{};
   a.pitch = (int)ckpt_pitch(K * T);

@@ -66,30 +66,41 @@ struct BwdwReduceArgs {
   Twiddles tw;
 };
 
-// Thread `idx` of one matrix's transform: channel idx % Kpad, half and k-step above it.
+// Thread `idx` of one matrix's transform: channel idx % Kmap, half and k-step above it.  Kmap is
+// Kpad (padding units written as zeros) or K (left as they are: the GEMMs' products with them
+// only reach gradient entries that are discarded).
 template <int T, typename Elt>
-__device__ __forceinline__ void spec_thread(const Elt* m, void* outUnits, int N, int K, int Kpad, int kgCount, size_t idx,
-                                            const Twiddles& tw) {
+__device__ __forceinline__ void spec_thread(const Elt* m, void* outUnits, int N, int K, int Kpad, int Kmap, int kgCount,
+                                            size_t idx, const Twiddles& tw) {
   using E = EltT<Elt>;
   constexpr int G = E::kPerUnit;
-  if (idx >= (size_t)kgCount * 2 * Kpad) return;
-  const int k = (int)(idx % Kpad);
-  const size_t rest = idx / Kpad;
+  if (idx >= (size_t)kgCount * 2 * Kmap) return;
+  const int k = (int)(idx % Kmap);
+  const size_t rest = idx / Kmap;
   const int half = (int)(rest & 1);
   const int kg = (int)(rest >> 1);
   const int row0 = kg * 2 * G + half * G;
+  const int rows = k < K ? min(G, N - row0) : 0;  // rows of this thread that exist
+  // Every row's load before the first transform: one wait for all of them instead of one each.
+  float v[G][T];
+  const Elt* src = m + ((size_t)row0 * K + k) * T;
+  const size_t pitch = (size_t)K * T;
+  if (rows >= G) {
+#pragma unroll
+    for (int e = 0; e < G; ++e) load_group<T, Elt>(src + e * pitch, v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+#pragma unroll
+      for (int h = 0; h < T; ++h) v[e][h] = 0.0f;
+      if (e < rows) load_group<T, Elt>(src + e * pitch, v[e]);
+    }
+  }
   float pl[T][G];
 #pragma unroll
   for (int e = 0; e < G; ++e) {
-    float v[T], o[T];
-    const int row = row0 + e;
-    if (row < N && k < K) {
-      load_group<T, Elt>(m + ((size_t)row * K + k) * T, v);
-    } else {
-#pragma unroll
-      for (int h = 0; h < T; ++h) v[h] = 0.0f;
-    }
-    Dft<T>::run(v, o, tw);
+    float o[T];
+    Dft<T>::run(v[e], o, tw);
 #pragma unroll
     for (int p = 0; p < T; ++p) pl[p][e] = o[p];
   }
@@ -104,8 +115,9 @@ template <int T, typename Elt>
 __global__ void __launch_bounds__(256) eql_spec_kernel(const SpecArgs a) {
   const bool second = (int)blockIdx.x >= a.blocks1;
   const size_t idx = (size_t)((int)blockIdx.x - (second ? a.blocks1 : 0)) * 256 + threadIdx.x;
+  const int Kpad = second ? a.Kpad2 : a.Kpad;
   spec_thread<T, Elt>(static_cast<const Elt*>(second ? a.m2 : a.m), second ? a.out2 : a.out, a.N, second ? a.K2 : a.K,
-                      second ? a.Kpad2 : a.Kpad, a.kgCount, idx, a.tw);
+                      Kpad, Kpad, a.kgCount, idx, a.tw);
 }
 
 // One item, as workgroup `block` of a launch of a.numItems.

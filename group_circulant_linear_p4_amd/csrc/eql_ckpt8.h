@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
 
 // x's half spectrum for the weight gradient, as eql_spec_kernel writes it, with the layer's
 // input rebuilt from a checkpoint: v = act(gamma[c] value + beta[c]).  The same launch can
-// transform dy, in blocks1 of its workgroups.
+// transform dy, in blocks1 of its workgroups.  Padding channels are left alone (spec_thread), so
+// narrow layers neither compute nor write them.
 struct Spec8Args {
   const unsigned char* codes;
   const unsigned char* scales;
@@ -343,18 +344,18 @@ __global__ void __launch_bounds__(256) eql_spec8_kernel(const Spec8Args a) {
   const uint32_t turn = blockIdx.x / kSpec8Turn, turns = gridDim.x / kSpec8Turn, dyTurns = a.blocks1 / kSpec8Turn;
   const uint32_t before = (uint32_t)((uint64_t)turn * dyTurns / turns);
   if ((uint32_t)((uint64_t)(turn + 1) * dyTurns / turns) > before) {
-    spec_thread<T, Elt>(static_cast<const Elt*>(a.m2), a.out2, a.N, a.K2, a.Kpad2, a.kgCount,
+    spec_thread<T, Elt>(static_cast<const Elt*>(a.m2), a.out2, a.N, a.K2, a.Kpad2, a.K2, a.kgCount,
                         (size_t)(before * kSpec8Turn + blockIdx.x % kSpec8Turn) * 256 + threadIdx.x, a.tw);
     return;
   }
   const size_t idx = (size_t)(blockIdx.x - before * kSpec8Turn) * 256 + threadIdx.x;
-  if (idx >= (size_t)a.kgCount * 2 * a.Kpad) return;
-  const int k = (int)(idx % a.Kpad);
-  const size_t rest = idx / a.Kpad;
+  if (idx >= (size_t)a.kgCount * 2 * a.K) return;
+  const int k = (int)(idx % a.K);
+  const size_t rest = idx / a.K;
   const int half = (int)(rest & 1);
   const int kg = (int)(rest >> 1);
   const int row0 = kg * 2 * G + half * G;
-  const int rows = k < a.K ? min(G, a.N - row0) : 0;  // rows of this thread that exist
+  const int rows = min(G, a.N - row0);  // rows of this thread that exist
   constexpr int WORDS = (T + 3) / 4;
   // A channel's T features lie in one block of 32 where T divides 32, else in at most two.
   constexpr bool ONE = kCkptBlock % T == 0;
