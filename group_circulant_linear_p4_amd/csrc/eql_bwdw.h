@@ -375,13 +375,13 @@ __global__ void __launch_bounds__(256) eql_bwdw_reduce(const BwdwReduceArgs a) {
 #pragma unroll
   for (int p = 0; p < T; ++p) P[p] = 0.0f;
   if (live) {
-#pragma unroll(UNROLL)
+#pragma unroll UNROLL
     for (int s = w; s < a.SR; s += WAVES) {
 #pragma unroll
       for (int p = 0; p < NR; ++p) P[p] += a.wsR[((size_t)s * NR + p) * plane + idx];
     }
     if constexpr (NC > 0) {
-#pragma unroll(UNROLL)
+#pragma unroll UNROLL
       for (int s = w; s < a.SP; s += WAVES) {
 #pragma unroll
         for (int p = 0; p < NC; ++p) P[NR + p] += a.wsP[((size_t)s * NC + p) * plane + idx];
