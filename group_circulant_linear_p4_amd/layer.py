@@ -460,18 +460,21 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
         dy2 = dy.reshape(N, Cp * T).to(dt).contiguous()
 
         def layer(g, w, ckpt, scale, shift, act, out, inp, need_w, need_x):
-            """Input and weight gradient of one layer (inp -> out channels) for output gradient g."""
+            """Input and weight gradient of one layer (inp -> out channels) for output gradient g.  At
+            p4 fp16 the input gradient's kernel can leave g's spectrum for the weight gradient; elsewhere
+            that would be a launch of its own, which eqlinear_bwd_w_ckpt8 shares with the checkpoint's."""
             dx = empty(N, inp * T) if need_x else None
             dw = torch.empty_like(w) if need_w else None
             n = eqlinear_bwd_w_workspace_bytes(N, inp, out, T, dt)
-            if need_w and need_x:
+            if need_w and need_x and T == 4 and dt == torch.float16:
                 ws = scratch(n)
                 eqlinear_ckpt8_spectrum(ckpt, scale, shift, act, ws, n, N, inp, out, T, dt)
                 eqlinear_bwd_x_train(g, _packed(w, EQL_PACK_BWDX), dx, ws, n, N, inp, out, T, dt)
                 eqlinear_bwd_w_train(g, dw, ws, n, N, inp, out, T, dt)
-            elif need_x:
+                return dx, dw
+            if need_x:
                 eqlinear_bwd_x(g, _packed(w, EQL_PACK_BWDX), dx, N, inp, out, T, dt)
-            elif need_w:
+            if need_w:
                 eqlinear_bwd_w_ckpt8(ckpt, scale, shift, act, g, dw, scratch(n), n, N, inp, out, T, dt)
             return dx, dw
 
