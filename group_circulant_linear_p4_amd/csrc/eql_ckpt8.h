@@ -246,8 +246,9 @@ struct Epi8Args {
   const unsigned char* scales;
   void* dpre;  // may be dy
   float* part; // [rowBlocks][R] or null
+  void* dbias; // [R / T]: written by the kernel itself (one row block), or null
   int64_t N;
-  int R, pitch, lanes, groups, colBlocks, rowsPerBlock;
+  int R, T, pitch, lanes, groups, colBlocks, rowsPerBlock;
 };
 constexpr int kEpi8Threads = 1024;
 
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
     if (r < r1) load(r);
     row_step(g0, w0, sc0, at);
   }
-  if (!a.part) return;
+  if (!a.part && !a.dbias) return;
   int half = 1;
   while (half < a.groups) half *= 2;
 #pragma unroll
@@ -306,10 +307,22 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
       for (int e = 0; e < 8; ++e) red[e][threadIdx.x] += red[e][threadIdx.x + half * a.lanes];
     }
   }
-  if (grp == 0 && n > 0) {
+  if (a.part) {
+    if (grp == 0 && n > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = red[e][threadIdx.x];
-    store_chunk8<float, WHOLE>(a.part + (int64_t)rb * a.R + f0, n, s);
+      for (int e = 0; e < 8; ++e) s[e] = red[e][threadIdx.x];
+      store_chunk8<float, WHOLE>(a.part + (int64_t)rb * a.R + f0, n, s);
+    }
+    return;
+  }
+  // One row block: the column block's channels are whole (the host sees to it), each the sum of
+  // its T features.
+  __syncthreads();
+  const int first = cb * a.lanes * 8, channels = min(a.lanes * 8, a.R - first) / a.T;
+  for (int c = (int)threadIdx.x; c < channels; c += kEpi8Threads) {
+    float t = 0.0f;
+    for (int j = c * a.T; j < (c + 1) * a.T; ++j) t += red[j & 7][j >> 3];
+    static_cast<Elt*>(a.dbias)[first / a.T + c] = (Elt)t;
   }
 }
 

@@ -285,7 +285,8 @@ def test_non_finite_rows_stay_in_their_rows():
 
 
 GELU_SHAPES = [(1, 1, 1), (3, 8, 4), (197, 384, 4), (501, 171, 3), (64, 133, 5), (2500, 16, 1), (30, 700, 3), (9, 2051, 4),
-               (3001, 40, 4), (700, 300, 7), (20, 900, 16)]
+               (3001, 40, 4), (700, 300, 7), (20, 900, 16),
+               (64, 700, 4), (65, 700, 4), (33, 640, 5), (17, 100, 16), (64, 2100, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
