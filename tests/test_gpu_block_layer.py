@@ -182,3 +182,37 @@ def test_example_trains():
     assert all(last < 0.7 * first for first, last in losses)
     # The same task with rounded and whole activations: the same descent to a few per cent.
     assert abs(losses[0][1] - losses[1][1]) <= 0.04 * losses[1][1]
+
+
+@pytest.mark.parametrize("ckpt8", [False, True])
+def test_mlp_block_gradient_against_differences(ckpt8):
+    """Directional derivatives of the block in x and in every parameter, fp32: central differences
+    (error: third derivative times step^2 / 6 and fp32 rounding of the outputs over the step, 2e-3
+    of the product of norms), and 4% of the gradient's norm along the direction with 8 bits."""
+    block = make_block(12, 20, 4, "f32", ckpt8, seed=5)
+    x = torch.randn(64, 48, device=DEV, requires_grad=True)
+    dy = torch.randn(64, 48, device=DEV)
+    block(x).backward(dy)
+    step = 1e-2
+    for name, p in [("x", x), *params(block).items()]:
+        v = torch.randn_like(p)
+        v /= v.norm()
+        with torch.no_grad():
+            p.add_(step * v)
+            hi = (block(x).double() * dy.double()).sum()
+            p.sub_(2 * step * v)
+            lo = (block(x).double() * dy.double()).sum()
+            p.add_(step * v)
+        got = (p.grad.double() * v.double()).sum().item()
+        slack = (0.04 if ckpt8 else 2e-3) * p.grad.norm().item() + 2e-3 * dy.norm().item()
+        assert abs(((hi - lo) / (2 * step)).item() - got) <= slack, name
+
+
+def test_default_stream_argument_is_torchs_current_stream():
+    import group_circulant_linear_p4_amd as eql
+    torch.cuda.init()
+    assert (eql._stream(None) or 0) == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert eql._stream(None) == side.cuda_stream == torch.cuda.current_stream().cuda_stream
+    assert (eql._stream(None) or 0) == torch.cuda.current_stream().cuda_stream
