@@ -362,6 +362,13 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[i][e] = ((float)xN[i][e] - meanN) * rstd;
+        int n = a.R - (lane + i * LPR) * 8;
+        if (a.R < (i + 1) * LPR * 8) {
+          // Missing features count as zero: mean rstd may overflow where no h does.
+          asm volatile("" : "+v"(n));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[i][e] = (WHOLE ? n > 0 : e < n) ? h[i][e] : 0.0f;
+        }
       }
     }
     if (base + step < a.N) load(row + step);
@@ -369,8 +376,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
     for (int i = 0; i < K; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        // Past the row's end dy is zero, and so are its products (h is finite there only if the
-        // row's statistics are, but such a row is NaN throughout anyway).
+        // Past the row's end dy and h are zero.
         const float d = (float)dy[i][e];
         const float g = d * (float)gam[i][e];
         s[0] += g;
@@ -549,7 +555,7 @@ __device__ __forceinline__ void wide_h(const NormArgs& a, int64_t row, int f0, i
   } else {
     const auto u = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = ((float)u[e] - mean) * rstd;
+    for (int e = 0; e < 8; ++e) h[e] = e < n ? ((float)u[e] - mean) * rstd : 0.0f;
   }
 }
 

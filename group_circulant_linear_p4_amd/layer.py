@@ -331,6 +331,12 @@ class EQLinearP4M(torch.nn.Module):
         return "in_channels=%d, out_channels=%d, group=p4m" % (self.in_channels, self.out_channels)
 
 
+def _rows(t: torch.Tensor, features: int) -> torch.Tensor:
+    """t as contiguous rows on a 16-byte boundary (a slice of a larger tensor may start off one)."""
+    t = t.reshape(-1, features).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class EQLayerNormFunction(torch.autograd.Function):
     """Layer norm of rows of C'*T features with one weight and bias per channel, shared by its
     T group elements (include/eqlinear_block.h).  Kept for the backward: x and the rows'
@@ -350,7 +356,7 @@ class EQLayerNormFunction(torch.autograd.Function):
                                  "shape %s" % (name, Cp, tuple(p.shape)))
             if p.dtype != x.dtype or p.device != x.device:
                 raise ValueError("x and %s must share a dtype (fp16 or fp32) and a device" % name)
-        x2 = x.reshape(-1, R).contiguous()
+        x2 = _rows(x, R)
         N = x2.shape[0]
         gamma, beta = (None if p is None else p.contiguous() for p in (gamma, beta))
         y = torch.empty_like(x2)
@@ -369,7 +375,7 @@ class EQLayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy: torch.Tensor):
         x2, ckpt, mean, rstd, gamma = ctx.saved_tensors
         N, Cp, T = ctx.sizes
-        dy2 = dy.reshape(N, Cp * T).to(ctx.dtype).contiguous()
+        dy2 = _rows(dy.to(ctx.dtype), Cp * T)
         dx = torch.empty_like(dy2)
         param = lambda: torch.empty(Cp, dtype=ctx.dtype, device=dy2.device)  # noqa: E731
         dg = param() if gamma is not None and ctx.needs_input_grad[1] else None
@@ -429,7 +435,7 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
                 raise ValueError("%s must be 1-D with %d values, got shape %s" % (name, n, tuple(p.shape)))
         if any(p.dtype != x.dtype or p.device != x.device for p in (gamma, beta, w1, b1, w2, b2)):
             raise ValueError("x and the block's parameters must share a dtype (fp16 or fp32) and a device")
-        x2 = x.reshape(-1, Cp * T).contiguous()
+        x2 = _rows(x, Cp * T)
         gamma, beta, w1, b1, w2, b2 = (p.contiguous() for p in (gamma, beta, w1, b1, w2, b2))
         N, dt, dev = x2.shape[0], x.dtype, x.device
         train = grad_mode and any(ctx.needs_input_grad[:7])
@@ -457,7 +463,7 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         empty = lambda *s: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
         scratch = lambda n: torch.empty(max(n, 16), dtype=torch.uint8, device=dev)  # noqa: E731
-        dy2 = dy.reshape(N, Cp * T).to(dt).contiguous()
+        dy2 = _rows(dy.to(dt), Cp * T)
 
         def layer(g, w, ckpt, scale, shift, act, out, inp, need_w, need_x):
             """Input and weight gradient of one layer (inp -> out channels) for output gradient g.  At

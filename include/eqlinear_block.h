@@ -43,7 +43,8 @@ extern "C" {
  */
 size_t eqlinear_ckpt8_bytes(int64_t N, int64_t Cp, int T);
 
-/* x: [N][Cp*T] read; ckpt: eqlinear_ckpt8_bytes(N, Cp, T) bytes written. */
+/* x: [N][Cp*T] read; ckpt: eqlinear_ckpt8_bytes(N, Cp, T) bytes written.  N P <= 2^35 - 2^11 here and
+ * in eqlinear_ckpt8_unpack (EQL_EINVAL otherwise). */
 int eqlinear_ckpt8_pack(const void* x, void* ckpt, int64_t N, int64_t Cp, int T, int dtype, void* stream);
 
 /* ckpt read; x: [N][Cp*T] written (the values, rounded to `dtype`: exact in fp32, and in fp16
@@ -63,7 +64,8 @@ int eqlinear_ckpt8_unpack(const void* ckpt, void* x, int64_t N, int64_t Cp, int 
  * mean, rstd: [N] floats, or NULL (4-byte aligned); the backward pass needs rstd, and mean
  *   unless it reads the checkpoint.
  * eps: >= 0 and finite, else EQL_EINVAL.  A row that holds an infinity or a NaN, or whose
- *   squares overflow fp32, or a constant row with eps = 0, gives NaN throughout.
+ *   squares overflow fp32, or whose var + eps is 0 or below fp32's normal range, gives NaN
+ *   throughout.
  * Rows over 16384 features take N <= 2^22 - 1 (EQL_EINVAL otherwise).
  */
 int eqlinear_layernorm_fwd(const void* x, const void* gamma, const void* beta, void* y, void* ckpt, float* mean,

@@ -284,6 +284,25 @@ def test_non_finite_rows_stay_in_their_rows():
         assert torch.isnan(dg).all().item() and torch.isfinite(db).all().item()
 
 
+@pytest.mark.parametrize("shape", [(3, 4, 1), (5, 8, 1), (9, 24, 4), (6, 13, 1), (2, 8193, 1), (2, 10000, 1)], ids=str)
+def test_constant_rows_of_large_values(shape):
+    """h is zero, though mean rstd is beyond fp32: y = beta, dx = rstd (g - mean(g))."""
+    n, c, t = shape
+    r, eps, f32 = c * t, 1e-12, eql.EQL_F32
+    g = np.random.default_rng(c)
+    dy = g.standard_normal((n, r)).astype(np.float32)
+    gamma, beta = (g.standard_normal(c).astype(np.float32) for _ in range(2))
+    x, y = torch.full((n, r), 2.0 ** 110, dtype=torch.float32, device=DEV), torch.empty((n, r), device=DEV)
+    mean, rstd = (torch.empty(n, dtype=torch.float32, device=DEV) for _ in range(2))
+    eql.eqlinear_layernorm_fwd(x, dev(gamma), dev(beta), y, None, mean, rstd, n, c, t, eps, f32)
+    assert np.array_equal(y.cpu().numpy(), np.broadcast_to(np.repeat(beta, t), (n, r)))
+    dx, dg, db = run_norm_bwd(dev(dy), x, mean, rstd, dev(gamma), None, "f32", c, t)
+    rdx, _, rdb = B.norm_bwd(dy, np.zeros((n, r)), np.full(n, 1e6), gamma, t, None)
+    close(dx, rdx, F32ERR * 1e6 * np.abs(dy * np.repeat(gamma, t)).max(), "f32")
+    assert not dg.any().item()
+    close(db, rdb, F32ERR * np.abs(dy).sum(), "f32")
+
+
 GELU_SHAPES = [(1, 1, 1), (3, 8, 4), (197, 384, 4), (501, 171, 3), (64, 133, 5), (2500, 16, 1), (30, 700, 3), (9, 2051, 4),
                (3001, 40, 4), (700, 300, 7), (20, 900, 16),
                (64, 700, 4), (65, 700, 4), (33, 640, 5), (17, 100, 16), (64, 2100, 1)]

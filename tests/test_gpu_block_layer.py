@@ -216,3 +216,22 @@ def test_default_stream_argument_is_torchs_current_stream():
     with torch.cuda.stream(side):
         assert eql._stream(None) == side.cuda_stream == torch.cuda.current_stream().cuda_stream
     assert (eql._stream(None) or 0) == torch.cuda.current_stream().cuda_stream
+
+
+def test_layers_take_slices_off_a_16_byte_boundary():
+    """Rows of 15 fp16 features: a slice from row 1 on starts 30 bytes into its tensor, and so does
+    the gradient that torch.cat's backward hands to the second of two."""
+    torch.manual_seed(4)
+    norm = EQLayerNorm(5, 3, device=DEV, dtype=torch.float16)
+    block = make_block(5, 7, 3, "f16", True)
+    whole = torch.randn(9, 15, device=DEV, dtype=torch.float16)
+    dy = torch.randn(9, 15, device=DEV, dtype=torch.float16)
+    for f in (norm, block):
+        grads = []
+        for part, start in ((whole[1:], 14), (whole[1:].clone(), 0)):
+            x = part.detach().requires_grad_(True)
+            assert x.data_ptr() % 16 == start
+            f.zero_grad()
+            torch.cat([whole[:1], f(x)]).backward(dy)
+            grads.append([x.grad] + [p.grad.clone() for p in f.parameters()])
+        assert all(torch.equal(a, b) for a, b in zip(*grads))
