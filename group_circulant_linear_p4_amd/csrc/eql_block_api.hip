@@ -25,7 +25,7 @@ bool streams(int64_t bytes) { return bytes > (256LL << 20); }
 
 // Workgroups of 1024 threads that the GELU backward aims at: one per compute unit.  More do not
 // read faster (N = 12608, R = 1536 fp16: 20.4 us with 256, 20.3 with 512; N = 65536, R = 4096: 242 and
-// 252) and leave more partial sums (the bias kernel after them 5.6 and 7.8 us).
+// 252) and leave more partial sums to add.
 constexpr int64_t kEpi8Workgroups = 256;
 
 // Workgroups for `turns` turns of a grid-stride loop: at most `most`, all with the same number
@@ -150,6 +150,7 @@ int norm_bwd(bool fromCkpt, const void* dy, const void* x, const void* ckpt, con
   q.C = (int)Cp;
   q.F = p.wide ? T : 1;
   q.groups = (int)ceil_div(Cp, 16);
+  q.blockStride = 2 * Cp * q.F;
   return status_of(launch_norm_param(f16, q, s));
 }
 
@@ -269,7 +270,7 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   a.T = T;
   // Up to 32 rows are one row block, whose workgroups write the bias gradient themselves where
   // their column blocks hold whole channels: one launch instead of two (9 rows of 240 fp32: 8.4 ->
-  // 5.6 us; 64 rows of 3600 would take 9.4 in one and 8.5 in two).
+  // 5.6 us; 64 rows of 3600 would take 9.4 in one and 7.8 in two).
   if (N <= 32) rowsPerBlock = 32;
   rowBlocks = ceil_div(N, rowsPerBlock);
   // Chunks across a workgroup: the row's chunks spread evenly over column blocks, which leaves room
@@ -283,7 +284,10 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   a.colBlocks = (int)ceil_div(chunks, a.lanes);
   rowsPerBlock = std::max(rowsPerBlock, ceil_div(N, std::max<int64_t>(1, kEpi8Workgroups / a.colBlocks)));
   rowBlocks = ceil_div(N, rowsPerBlock);
-  const bool direct = parts && rowBlocks == 1 && (a.colBlocks == 1 || a.lanes * 8 % T == 0);
+  // Column blocks of whole channels add a channel's T features themselves: T times fewer partial
+  // sums for the second launch (5003 rows of 513, T = 3 fp16: 12.5 -> 10.3 us).
+  a.fold = a.colBlocks == 1 || a.lanes * 8 % T == 0;
+  const bool direct = parts && rowBlocks == 1 && a.fold;
   a.part = parts && !direct ? static_cast<float*>(workspace) : nullptr;
   a.dbias = direct ? dbias : nullptr;
   a.groups = (int)std::min<int64_t>(kEpi8Threads / a.lanes, rowsPerBlock);
@@ -293,6 +297,17 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   const bool f16 = dtype == EQL_F16;
   if (N > 0 && launch_epi8(f16, streams(N * (int64_t)a.R * (2 * elt_bytes(dtype) + 1)), a, (unsigned)(rowBlocks * a.colBlocks), s) != hipSuccess) return EQL_EHIP;
   if (!dbias || direct) return EQL_OK;
+  if (a.fold) {
+    NormParamArgs q{};
+    q.part = a.part;
+    q.dgamma = dbias;
+    q.blocks = N > 0 ? (int)rowBlocks : 0;  // 0 without rows: a zero gradient
+    q.C = (int)Dp;
+    q.F = 1;
+    q.groups = (int)ceil_div(Dp, 16);
+    q.blockStride = Dp;
+    return status_of(launch_norm_param(f16, q, s));
+  }
   EpiBwdArgs b{};
   b.part = a.part;
   b.dbias = dbias;
@@ -300,7 +315,7 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   b.Dp = (int)Dp;
   b.T = T;
   b.rowElems = a.R;
-  b.rowBlocks = N > 0 ? (int)rowBlocks : 0;  // 0 without rows: a zero gradient
+  b.rowBlocks = N > 0 ? (int)rowBlocks : 0;
   return status_of(launch_epi_bias(f16, b, (unsigned)ceil_div(Dp, 16), s));
 }
 

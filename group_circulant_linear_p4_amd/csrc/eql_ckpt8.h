@@ -245,10 +245,11 @@ struct Epi8Args {
   const unsigned char* codes;
   const unsigned char* scales;
   void* dpre;  // may be dy
-  float* part; // [rowBlocks][R] or null
-  void* dbias; // [R / T]: written by the kernel itself (one row block), or null
+  float* part; // [rowBlocks][R], or with fold [rowBlocks][R / T], or null
+  void* dbias; // [R / T]: written by the kernel itself (one row block, fold), or null
   int64_t N;
   int R, T, pitch, lanes, groups, colBlocks, rowsPerBlock;
+  int fold;    // 1: column blocks hold whole channels, whose T features are added here
 };
 constexpr int kEpi8Threads = 1024;
 
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
       for (int e = 0; e < 8; ++e) red[e][threadIdx.x] += red[e][threadIdx.x + half * a.lanes];
     }
   }
-  if (a.part) {
+  if (!a.fold) {
     if (grp == 0 && n > 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] = red[e][threadIdx.x];
@@ -315,14 +316,13 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
     }
     return;
   }
-  // One row block: the column block's channels are whole (the host sees to it), each the sum of
-  // its T features.
   __syncthreads();
-  const int first = cb * a.lanes * 8, channels = min(a.lanes * 8, a.R - first) / a.T;
+  const int first = cb * a.lanes * 8, channels = min(a.lanes * 8, a.R - first) / a.T, c0 = first / a.T;
   for (int c = (int)threadIdx.x; c < channels; c += kEpi8Threads) {
     float t = 0.0f;
     for (int j = c * a.T; j < (c + 1) * a.T; ++j) t += red[j & 7][j >> 3];
-    static_cast<Elt*>(a.dbias)[first / a.T + c] = (Elt)t;
+    if (a.part) a.part[(int64_t)rb * (a.R / a.T) + c0 + c] = t;
+    else static_cast<Elt*>(a.dbias)[c0 + c] = (Elt)t;
   }
 }
 

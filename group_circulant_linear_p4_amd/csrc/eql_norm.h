@@ -433,13 +433,14 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
 }
 
 // dgamma and dbeta from the blocks' column sums part[b][2][C * F] (F features a channel left to
-// add): a workgroup takes 16 channels x 16 slices of the blocks, slice l blocks l, l + 16, ...;
+// add), or one gradient from part[b][C]: a workgroup takes 16 channels x 16 slices of the blocks, slice l blocks l, l + 16, ...;
 // the slices are added in order and the result rounded once.
 struct NormParamArgs {
   const float* part;
   void* dgamma;  // [C] or null
   void* dbeta;   // [C] or null
   int blocks, C, F, groups;  // groups = ceil(C / 16); workgroups groups .. 2 groups - 1: dbeta
+  int64_t blockStride;       // floats from a block's sums to the next one's
 };
 
 template <typename Elt>
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(256) eql_norm_param_kernel(const NormParamArgs
       for (int f = 0; f < a.F; ++f) {
         float t[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) t[u] = b + 16 * u < a.blocks ? p[(b + 16 * u) * 2 * stride + f] : 0.0f;
+        for (int u = 0; u < 8; ++u) t[u] = b + 16 * u < a.blocks ? p[(b + 16 * u) * a.blockStride + f] : 0.0f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) s += t[u];
       }
