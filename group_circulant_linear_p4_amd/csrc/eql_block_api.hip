@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "eql_block.h"
 #include "eqlinear_block.h"
@@ -268,26 +269,26 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   a.codes = static_cast<const unsigned char*>(pre_ckpt);
   a.scales = a.codes ? a.codes + N * a.pitch : nullptr;
   a.T = T;
-  // Up to 32 rows are one row block, whose workgroups write the bias gradient themselves where
-  // their column blocks hold whole channels: one launch instead of two (9 rows of 240 fp32: 8.4 ->
-  // 5.6 us; 64 rows of 3600 would take 9.4 in one and 7.8 in two).
+  // Up to 32 rows are one row block, whose workgroups write the bias gradient themselves: one
+  // launch instead of two (9 rows of 240 fp32: 8.4 -> 5.6 us; 64 rows of 3600 would take 9.4 in one
+  // and 7.8 in two).
   if (N <= 32) rowsPerBlock = 32;
   rowBlocks = ceil_div(N, rowsPerBlock);
   // Chunks across a workgroup: the row's chunks spread evenly over column blocks, which leaves room
   // for 1024 / lanes rows at a time.  As few column blocks as hold the row, or more (down to 32
   // lanes) until there is a workgroup per compute unit; then row blocks as tall as keep it so,
-  // each leaving one sum a feature to add (and no more of them than the workspace is sized for).
+  // each leaving one sum a channel to add (and no more of them than the workspace is sized for).
   const int64_t chunks = ceil_div(a.R, 8);
   int64_t colBlocks = ceil_div(chunks, kEpi8Threads);
   while (rowBlocks * colBlocks < kEpi8Workgroups && ceil_div(chunks, 2 * colBlocks) >= 32) colBlocks *= 2;
-  a.lanes = (int)ceil_div(chunks, colBlocks);
+  // Whole channels in each: they add a channel's T features themselves, T times fewer partial sums
+  // for the second launch (5003 rows of 513, T = 3 fp16: 12.5 -> 10.3 us).
+  const int64_t whole = colBlocks == 1 ? 1 : T / std::gcd(T, 8);
+  a.lanes = (int)std::min(ceil_div(ceil_div(chunks, colBlocks), whole), kEpi8Threads / whole) * (int)whole;
   a.colBlocks = (int)ceil_div(chunks, a.lanes);
   rowsPerBlock = std::max(rowsPerBlock, ceil_div(N, std::max<int64_t>(1, kEpi8Workgroups / a.colBlocks)));
   rowBlocks = ceil_div(N, rowsPerBlock);
-  // Column blocks of whole channels add a channel's T features themselves: T times fewer partial
-  // sums for the second launch (5003 rows of 513, T = 3 fp16: 12.5 -> 10.3 us).
-  a.fold = a.colBlocks == 1 || a.lanes * 8 % T == 0;
-  const bool direct = parts && rowBlocks == 1 && a.fold;
+  const bool direct = parts && rowBlocks == 1;
   a.part = parts && !direct ? static_cast<float*>(workspace) : nullptr;
   a.dbias = direct ? dbias : nullptr;
   a.groups = (int)std::min<int64_t>(kEpi8Threads / a.lanes, rowsPerBlock);
@@ -297,26 +298,15 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
   const bool f16 = dtype == EQL_F16;
   if (N > 0 && launch_epi8(f16, streams(N * (int64_t)a.R * (2 * elt_bytes(dtype) + 1)), a, (unsigned)(rowBlocks * a.colBlocks), s) != hipSuccess) return EQL_EHIP;
   if (!dbias || direct) return EQL_OK;
-  if (a.fold) {
-    NormParamArgs q{};
-    q.part = a.part;
-    q.dgamma = dbias;
-    q.blocks = N > 0 ? (int)rowBlocks : 0;  // 0 without rows: a zero gradient
-    q.C = (int)Dp;
-    q.F = 1;
-    q.groups = (int)ceil_div(Dp, 16);
-    q.blockStride = Dp;
-    return status_of(launch_norm_param(f16, q, s));
-  }
-  EpiBwdArgs b{};
-  b.part = a.part;
-  b.dbias = dbias;
-  b.N = (int)N;
-  b.Dp = (int)Dp;
-  b.T = T;
-  b.rowElems = a.R;
-  b.rowBlocks = N > 0 ? (int)rowBlocks : 0;
-  return status_of(launch_epi_bias(f16, b, (unsigned)ceil_div(Dp, 16), s));
+  NormParamArgs q{};
+  q.part = a.part;
+  q.dgamma = dbias;
+  q.blocks = N > 0 ? (int)rowBlocks : 0;  // 0 without rows: a zero gradient
+  q.C = (int)Dp;
+  q.F = 1;
+  q.groups = (int)ceil_div(Dp, 16);
+  q.blockStride = Dp;
+  return status_of(launch_norm_param(f16, q, s));
 }
 
 int eqlinear_ckpt8_spectrum(const void* ckpt, const void* gamma, const void* beta, int act, void* workspace,

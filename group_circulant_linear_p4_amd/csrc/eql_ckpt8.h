@@ -236,20 +236,19 @@ __global__ void __launch_bounds__(256) eql_ckpt_unpack_kernel(const CkptArgs a) 
 }
 
 // Backward of the bias + GELU epilogue with GELU's input read from a checkpoint:
-//     dpre = dy GELU'(value),   part[row block][feature] = sum over the block's rows of dpre.
+//     dpre = dy GELU'(value),   part[row block][channel] = sum over the block's rows and t of dpre.
 // A workgroup of 1024 threads takes `lanes` chunks across and `groups` = 1024 / lanes rows at a
 // time down its block of rows, the next rows' operands in flight; the column sums of its row
-// groups are added pairwise through LDS.
+// groups are added pairwise through LDS, then the T of each channel.
 struct Epi8Args {
   const void* dy;
   const unsigned char* codes;
   const unsigned char* scales;
   void* dpre;  // may be dy
-  float* part; // [rowBlocks][R], or with fold [rowBlocks][R / T], or null
-  void* dbias; // [R / T]: written by the kernel itself (one row block, fold), or null
+  float* part; // [rowBlocks][R / T], or null
+  void* dbias; // [R / T]: written by the kernel itself (one row block), or null
   int64_t N;
   int R, T, pitch, lanes, groups, colBlocks, rowsPerBlock;
-  int fold;    // 1: column blocks hold whole channels, whose T features are added here
 };
 constexpr int kEpi8Threads = 1024;
 
@@ -308,14 +307,7 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
       for (int e = 0; e < 8; ++e) red[e][threadIdx.x] += red[e][threadIdx.x + half * a.lanes];
     }
   }
-  if (!a.fold) {
-    if (grp == 0 && n > 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = red[e][threadIdx.x];
-      store_chunk8<float, WHOLE>(a.part + (int64_t)rb * a.R + f0, n, s);
-    }
-    return;
-  }
+  // Column blocks hold whole channels (lanes * 8 is a multiple of T, or there is one block).
   __syncthreads();
   const int first = cb * a.lanes * 8, channels = min(a.lanes * 8, a.R - first) / a.T, c0 = first / a.T;
   for (int c = (int)threadIdx.x; c < channels; c += kEpi8Threads) {
