@@ -322,6 +322,10 @@ __global__ void __launch_bounds__(kEpi8Threads) eql_epi8_kernel(const Epi8Args a
 // input rebuilt from a checkpoint: v = act(gamma[c] value + beta[c]).  The same launch can
 // transform dy, in blocks1 of its workgroups.  Padding channels are left alone (spec_thread), so
 // narrow layers neither compute nor write them.
+// The transform is fp32; the spectrum is rounded to the element type once, since that is what the
+// GEMM's matrix instructions take: with dy's it leaves an fp16 gradient 3.7 to 4.0e-4 of its norm
+// off, where its own last rounding alone is 2.1e-4.  Carrying a remainder beside one operand would
+// double the products (N = 65536, 1024 x 1024 channels: 710 us of GEMM more).
 struct Spec8Args {
   const unsigned char* codes;
   const unsigned char* scales;

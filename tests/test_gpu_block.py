@@ -305,7 +305,9 @@ def test_constant_rows_of_large_values(shape):
 
 GELU_SHAPES = [(1, 1, 1), (3, 8, 4), (197, 384, 4), (501, 171, 3), (64, 133, 5), (2500, 16, 1), (30, 700, 3), (9, 2051, 4),
                (3001, 40, 4), (700, 300, 7), (20, 900, 16),
-               (64, 700, 4), (65, 700, 4), (33, 640, 5), (17, 100, 16), (64, 2100, 1)]
+               (64, 700, 4), (65, 700, 4), (33, 640, 5), (17, 100, 16), (64, 2100, 1),
+               # column blocks of whole channels at orders that do not divide 8
+               (100, 900, 7), (300, 601, 15), (40, 1200, 9), (35, 1367, 12), (600, 2733, 3), (1, 5461, 3), (50, 1, 13)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
