@@ -52,7 +52,7 @@ hipError_t launch_norm_bwd_wide(bool f16, bool ckpt, const NormArgs& a, unsigned
 
 hipError_t launch_norm_param(bool f16, const NormParamArgs& a, hipStream_t s) {
   return launch_kernel(f16 ? (const void*)&eql_norm_param_kernel<_Float16> : (const void*)&eql_norm_param_kernel<float>,
-                       (a.dbeta ? 2u : 1u) * (unsigned)a.groups, a, s);
+                       (a.dbeta ? 2u : 1u) * (unsigned)a.groups, a, s, 1024);
 }
 
 }  // namespace eql
