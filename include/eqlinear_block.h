@@ -64,7 +64,7 @@ int eqlinear_ckpt8_unpack(const void* ckpt, void* x, int64_t N, int64_t Cp, int 
  * mean, rstd: [N] floats, or NULL (4-byte aligned); the backward pass needs rstd, and mean
  *   unless it reads the checkpoint.
  * eps: >= 0 and finite, else EQL_EINVAL.  A row that holds an infinity or a NaN, or whose
- *   squares overflow fp32, or whose var + eps is 0 or below fp32's normal range, gives NaN
+ *   sum or squares overflow fp32, or whose var + eps is 0 or below fp32's normal range, gives NaN
  *   throughout.
  * Rows over 16384 features take N <= 2^22 - 1 (EQL_EINVAL otherwise).
  */

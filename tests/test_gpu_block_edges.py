@@ -1,0 +1,81 @@
+"""GPU tests of the block operators' edges (include/eqlinear_block.h): what the definitions give
+exactly, and results at the ends of the number ranges."""
+import numpy as np
+import pytest
+import torch
+
+import group_circulant_linear_p4_amd as eql
+from oracle import block_oracle as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+NP = {"f16": np.float16, "f32": np.float32}
+DT = {"f16": eql.EQL_F16, "f32": eql.EQL_F32}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def scratch(nbytes):
+    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=DEV)
+
+
+# Row lengths R whose rounded reciprocal is not their inverse, fl(R fl(1 / R)) != 1: on 16 and on 64
+# lanes and on a whole workgroup, one to several chunks a lane, whole and ragged rows, group orders
+# with and without a table, and rows past the registers, backward (8192) and forward (16384).
+UNEVEN = [(41, 1), (41, 4), (55, 3), (94, 2), (82, 4), (332, 2), (23, 5), (141, 4), (2256, 1), (614, 4), (8437, 1),
+          (4331, 2), (16707, 1), (5774, 3), (3502, 5)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("shape", UNEVEN, ids=str)
+def test_constant_rows_have_no_deviation(shape, dtype):
+    """The sum of R equal features is exact here (integers below 2^24 times a power of two), so the
+    mean is the feature itself: h = 0, y = beta bit for bit, the checkpoint's codes are zero."""
+    c, t = shape
+    r, n = c * t, 5
+    assert np.float32(r) * np.float32(1.0 / r) != 1
+    g = np.random.default_rng(r)
+    beta, gamma = (g.standard_normal(c).astype(NP[dtype]) for _ in range(2))
+    for value in (1000.0, 16384.0) if dtype == "f16" else (1000.0, 16384.0, 2.0 ** 110):
+        x = torch.full((n, r), value, dtype=torch.float16 if dtype == "f16" else torch.float32, device=DEV)
+        y, ck = torch.empty_like(x), scratch(eql.eqlinear_ckpt8_bytes(n, c, t))
+        mean, rstd = (torch.empty(n, dtype=torch.float32, device=DEV) for _ in range(2))
+        eql.eqlinear_layernorm_fwd(x, dev(gamma), dev(beta), y, ck, mean, rstd, n, c, t, 1e-5, DT[dtype])
+        assert (mean == value).all().item()
+        assert np.array_equal(y.cpu().numpy(), np.broadcast_to(np.repeat(beta, t), (n, r)))
+        assert not ck[:n * (-(-r // 32) * 32)].any().item()
+
+
+@pytest.mark.parametrize("source", ["x", "ckpt"])
+@pytest.mark.parametrize("shape", UNEVEN, ids=str)
+def test_constant_gradients_of_constant_rows_vanish(shape, source):
+    """With h = 0 and equal g the input gradient rstd (g - mean(g)) is zero, and so is dgamma; dbeta
+    is the count."""
+    c, t = shape
+    r, n, f32 = c * t, 3, eql.EQL_F32
+    dy, dx = torch.ones((n, r), device=DEV), torch.full((n, r), 7.0, device=DEV)
+    x, mean, rstd = torch.full((n, r), 1000.0, device=DEV), torch.full((n,), 1000.0, device=DEV), torch.full((n,), 300.0, device=DEV)
+    dg, db = torch.full((c,), 7.0, device=DEV), torch.empty(c, device=DEV)
+    nbytes = eql.eqlinear_layernorm_bwd_workspace_bytes(n, c, t, f32)
+    ws = scratch(nbytes)
+    if source == "x":
+        eql.eqlinear_layernorm_bwd(dy, x, mean, rstd, None, None, dx, dg, db, ws, nbytes, n, c, t, f32)
+    else:
+        ck = dev(B.buffer(*B.pack(np.zeros((n, r)))))
+        eql.eqlinear_layernorm_bwd_ckpt8(dy, ck, rstd, None, None, dx, dg, db, ws, nbytes, n, c, t, f32)
+    assert not dx.any().item() and not dg.any().item() and (db == n * t).all().item()
+
+
+@pytest.mark.parametrize("shape", [(41, 4), (16707, 1)], ids=str)
+def test_rows_whose_sum_overflows_are_nan(shape):
+    """The other rows are not touched by it."""
+    c, t = shape
+    n, r = 4, c * t
+    x = torch.randn(n, r, device=DEV)
+    x[2] = 3e38
+    y = torch.empty_like(x)
+    eql.eqlinear_layernorm_fwd(x, None, None, y, None, None, None, n, c, t, 1e-5, eql.EQL_F32)
+    assert torch.isnan(y[2]).all().item() and torch.isfinite(y[[0, 1, 3]]).all().item()
