@@ -5,7 +5,10 @@
 // of 32 consecutive features of a row (the last one may be short) share one power-of-two step,
 //     a = max |v| over the block,  e = the smallest integer >= -126 with a 2^-e < 127.5,
 //     code = v 2^-e rounded to nearest even, in [-127, 127],   value = code 2^e,
-// so the error is at most half a step, 2^(e-1) <= a / 127.  A power-of-two step makes both
+// so the error is at most half a step, 2^(e-1) <= a / 127.  e stops at 121 (fp16 matrices: 9), the
+// largest step of which the type holds 127: a block that would take the next one (a of 127.5 2^121
+// or more; 65280 or more) keeps this one, its largest values become +-127 steps, still within
+// a / 127, and everything that reads it sees finite values.  A power-of-two step makes both
 // directions exact but for that one rounding: codes are the same whatever computed them, and a
 // code's value is exact in fp32 and, for values of ordinary size, in fp16.  A block that holds
 // an infinity or a NaN reads back as NaN throughout (a training step must not lose an
@@ -216,7 +219,14 @@ __global__ void __launch_bounds__(256) eql_ckpt_pack_kernel(const CkptArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu);
   top = quad_max(top);
-  const BlockStep st = block_step(top);
+  BlockStep st = block_step(top);
+  constexpr int last = sizeof(Elt) == 2 ? 9 : 121;  // the largest e
+  if (st.scale > last + 127u) {
+    constexpr float step = sizeof(Elt) == 2 ? 0x1p9f : 0x1p121f;
+    st = {1.0f / step, last + 127u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __builtin_fminf(__builtin_fmaxf(f[e], -127.0f * step), 127.0f * step);
+  }
   *reinterpret_cast<u32x2*>(a.codes + idx * 8) = encode8(f, st.back);
   if ((threadIdx.x & 3) == 0) a.scales[idx >> 2] = (unsigned char)(top >= 0x7F800000u ? 255u : st.scale);
 }

@@ -33,13 +33,15 @@ extern "C" {
 /*
  * 8-bit checkpoint of an [N][R] matrix.  32 consecutive features of a row (the row's last block
  * may be shorter) share one power-of-two step 2^e:
- *     e     the smallest integer >= -126 with max|v| 2^-e < 127.5 over the block
- *     code  v 2^-e rounded to nearest even, in [-127, 127];  value = code 2^e
- * The error is at most half a step (at most max|v| / 127); codes do not depend on how they are
- * computed.  A block with an infinity or a NaN reads back as NaN throughout.
+ *     e     the smallest integer >= -126 with max|v| 2^-e < 127.5 over the block, but at most 121
+ *           (9 where a fp16 matrix is packed): a block of finite values stays finite in its type
+ *     code  v 2^-e rounded to nearest even, held to [-127, 127];  value = code 2^e
+ * The error is at most half a step, or where the limit on e takes effect (max|v| of 127.5 2^121, in
+ * fp16 65280, or more) less than one; at most max|v| / 127 either way.  Codes do not depend on how
+ * they are computed.  A block with an infinity or a NaN reads back as NaN throughout.
  * Layout, with P = 32 ceil(R / 32): N rows of P signed bytes (codes; zero past R), then N rows
  * of P / 32 bytes e + 127 (255: the block is NaN, its codes are unspecified).  The size does not
- * depend on the element type, nor does the content for equal values.
+ * depend on the element type, nor does the content for equal values but for fp16's limit on e.
  */
 size_t eqlinear_ckpt8_bytes(int64_t N, int64_t Cp, int T);
 
@@ -48,7 +50,8 @@ size_t eqlinear_ckpt8_bytes(int64_t N, int64_t Cp, int T);
 int eqlinear_ckpt8_pack(const void* x, void* ckpt, int64_t N, int64_t Cp, int T, int dtype, void* stream);
 
 /* ckpt read; x: [N][Cp*T] written (the values, rounded to `dtype`: exact in fp32, and in fp16
- * for values that a fp16 matrix was packed from, or of ordinary size). */
+ * where a fp16 matrix was packed whose largest magnitude in the block is at least 2^-18 or so; a
+ * fp32 matrix's values may be beyond fp16's range). */
 int eqlinear_ckpt8_unpack(const void* ckpt, void* x, int64_t N, int64_t Cp, int T, int dtype, void* stream);
 
 /*

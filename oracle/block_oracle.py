@@ -36,9 +36,12 @@ def norm_bwd(dy, h, rstd, gamma, T, dres=None):
     return dx, per_channel(dy * h), per_channel(dy)
 
 
-def pack(x):
-    """(codes [N, P] int8, scale bytes [N, P / 32] uint8) of x [N, R]; the codes of a block with
-    an infinity or a NaN are given as zeros (the format leaves them open)."""
+LAST_STEP = {"f32": 121, "f16": 9}  # exponent of the largest step of which 127 are finite
+
+
+def pack(x, dtype="f32"):
+    """(codes [N, P] int8, scale bytes [N, P / 32] uint8) of x [N, R] in `dtype`; the codes of a block
+    with an infinity or a NaN are given as zeros (the format leaves them open)."""
     x = np.asarray(x, np.float64)
     n, r = x.shape
     p = -(-r // BLOCK) * BLOCK
@@ -53,8 +56,11 @@ def pack(x):
     e = np.where(top > 0, np.maximum(e, np.frexp(top)[1] - 9), e)
     for _ in range(4):
         e = np.where(top < np.ldexp(127.5, e), e, e + 1)
+    held = e > LAST_STEP[dtype]
+    e = np.minimum(e, LAST_STEP[dtype])
     codes = np.rint(np.ldexp(v, -e[..., None]))
-    assert np.abs(codes).max(initial=0) <= 127
+    assert np.abs(codes[~held]).max(initial=0) <= 127
+    codes = np.clip(codes, -127, 127)
     scale = np.where(finite, e + 127, 255).astype(np.uint8)
     return codes.astype(np.int8).reshape(n, p), scale
 

@@ -1,0 +1,24 @@
+"""CPU checks of the block operators' edges (oracle/block_oracle.py and include/eqlinear_block.h)."""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as B
+
+
+@pytest.mark.parametrize("dtype,last", [("f16", 9), ("f32", 121)])
+def test_checkpoint_of_the_largest_values(dtype, last):
+    """Steps stop where 127 of them are the type's last; values stay within 1 / 127 of the block's
+    largest, and one below that limit nothing changes."""
+    np_type = np.float16 if dtype == "f16" else np.float32
+    top = np.ldexp(127.5, last)
+    x = np.zeros((4, 32), np_type)
+    x[0, :3] = np.finfo(np_type).max, -np.finfo(np_type).max, np.ldexp(1.0, last + 5)
+    x[1, 0] = top
+    x[2, 0] = np.nextafter(np_type(top), np_type(0))
+    x[3, 0] = np.ldexp(1.0, last)
+    codes, scale = B.pack(x, dtype)
+    assert list(scale[:, 0]) == [last + 127, last + 127, last + 127, last + 127 - 6]
+    assert list(codes[0, :3]) == [127, -127, 32] and codes[1, 0] == codes[2, 0] == 127 and codes[3, 0] == 64
+    with np.errstate(over="raise"):
+        back = B.unpack(codes, scale, 32).astype(np_type)
+    assert (np.abs(back.astype(np.float64) - x) <= np.abs(x.astype(np.float64)).max(1, keepdims=True) / 127).all()

@@ -79,3 +79,46 @@ def test_rows_whose_sum_overflows_are_nan(shape):
     y = torch.empty_like(x)
     eql.eqlinear_layernorm_fwd(x, None, None, y, None, None, None, n, c, t, 1e-5, eql.EQL_F32)
     assert torch.isnan(y[2]).all().item() and torch.isfinite(y[[0, 1, 3]]).all().item()
+
+
+# Largest magnitudes of a block around the last one whose step the element type can hold.
+TOPS = {"f16": [65184.0, 65248.0, 65280.0, 65312.0, 65472.0, 65504.0],
+        "f32": [float(np.float32(v)) for v in (127.25 * 2.0 ** 121, np.nextafter(np.float32(127.5 * 2.0 ** 121), np.float32(0)),
+                                               127.5 * 2.0 ** 121, 127.9 * 2.0 ** 121, np.finfo(np.float32).max)]}
+
+
+@pytest.mark.parametrize("shape", [(3, 25, 4), (2, 32, 1), (5, 7, 5)], ids=str)
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_checkpoints_of_the_largest_finite_values(dtype, shape):
+    """Finite matrices come back finite, each value within 1 / 127 of its block's largest."""
+    n, c, t = shape
+    r = c * t
+    g = np.random.default_rng(r)
+    for top in TOPS[dtype]:
+        x = (top * g.uniform(-1, 1, (n, r))).astype(NP[dtype])
+        x[0, :] = -top
+        x[-1, ::3] = top
+        ck, back = scratch(eql.eqlinear_ckpt8_bytes(n, c, t)), dev(np.zeros_like(x))
+        eql.eqlinear_ckpt8_pack(dev(x), ck, n, c, t, DT[dtype])
+        eql.eqlinear_ckpt8_unpack(ck, back, n, c, t, DT[dtype])
+        got, x64 = back.cpu().numpy().astype(np.float64), x.astype(np.float64)
+        assert np.isfinite(got).all(), top
+        pad = np.zeros((n, -(-r // 32) * 32))
+        pad[:, :r] = np.abs(x64)
+        largest = np.repeat(pad.reshape(n, -1, 32).max(2), 32, axis=1)[:, :r]
+        assert (np.abs(got - x64) <= largest / 127).all(), top
+        codes, scale = B.pack(x, dtype)
+        raw, p = ck.cpu().numpy(), codes.shape[1]
+        assert np.array_equal(raw[:n * p].view(np.int8).reshape(n, p), codes)
+        assert np.array_equal(raw[n * p:n * (p + p // 32)].reshape(n, -1), scale)
+        # The passes that read a checkpoint see finite values too.
+        dy, dpre = dev(np.ones_like(x)), dev(np.zeros_like(x))
+        eql.eqlinear_fused_epilogue_bwd_ckpt8(dy, ck, dpre, None, None, 0, n, c, t, DT[dtype])
+        assert torch.isfinite(dpre).all().item()
+        if t == 1:  # one feature a channel: the spectrum is the input itself
+            d, nbytes = 3, eql.eqlinear_bwd_w_workspace_bytes(n, c, 3, t, DT[dtype])
+            e = np.zeros((n, d), NP[dtype])
+            e[0, 1] = e[1, 2] = 1
+            dw = torch.empty((d, c, t), dtype=back.dtype, device=DEV)
+            eql.eqlinear_bwd_w_ckpt8(ck, None, None, eql.EQL_ACT_NONE, dev(e), dw, scratch(nbytes), nbytes, n, c, d, t, DT[dtype])
+            assert np.array_equal(dw.cpu().numpy()[1:, :, 0], back.cpu().numpy()[:2])
