@@ -122,3 +122,61 @@ def test_checkpoints_of_the_largest_finite_values(dtype, shape):
             dw = torch.empty((d, c, t), dtype=back.dtype, device=DEV)
             eql.eqlinear_bwd_w_ckpt8(ck, None, None, eql.EQL_ACT_NONE, dev(e), dw, scratch(nbytes), nbytes, n, c, d, t, DT[dtype])
             assert np.array_equal(dw.cpu().numpy()[1:, :, 0], back.cpu().numpy()[:2])
+
+
+
+
+def plain_spectrum_f16(x, t):
+    """[T planes][N][C] as the transform computes them: sums over h in order, multiply-adds in fp32
+    with coefficients rounded to fp32, 0 and +-1 exact; the last multiply-add rounds to fp16 once, a
+    last addition to fp32 and then to fp16."""
+    n = x.shape[0]
+    v = x.astype(np.float32).reshape(n, -1, t).astype(np.longdouble)
+    cs = [np.longdouble(np.float32(np.cos(2 * np.pi * m / t))) for m in range(t)]
+    sn = [np.longdouble(np.float32(np.sin(2 * np.pi * m / t))) for m in range(t)]
+    real = 2 if t % 2 == 0 and t > 1 else 1
+    planes = []
+    for p in range(t):
+        k = 0 if p == 0 else (t // 2 if p < real else (p - real) // 2 + 1)
+        imag = p >= real and (p - real) & 1
+        terms = []  # (coefficient, needs a product)
+        for h in range(t):
+            m = h * k % t
+            if imag:
+                if m == 0 or 2 * m == t:
+                    continue
+                terms.append((h, -1.0, False) if 4 * m == t else (h, 1.0, False) if 4 * m == 3 * t else (h, -sn[m], True))
+            else:
+                if 4 * m == t or 4 * m == 3 * t:
+                    continue
+                terms.append((h, 1.0, False) if m == 0 else (h, -1.0, False) if 2 * m == t else (h, cs[m], True))
+        s = np.zeros(v.shape[:2], np.longdouble)
+        for i, (h, coeff, product) in enumerate(terms):
+            s = s + v[:, :, h] * coeff
+            last = i == len(terms) - 1
+            if not (last and product):
+                s = s.astype(np.float32)
+            # By way of fp64: from extended precision NumPy rounds to fp32 first.
+            s = s.astype(np.float64).astype(np.float16) if last else s.astype(np.longdouble)
+        planes.append(s)
+    return np.stack(planes)
+
+
+@pytest.mark.parametrize("t", [3, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16])
+def test_fp16_spectra_are_rounded_once(t):
+    """The spectrum that eqlinear_fwd_train leaves (first dy's section, then x's: units of eight rows
+    [k-step][plane][half][channel], channels padded to 64), bit for bit."""
+    n, c, d = 4096, 40, 3
+    g = np.random.default_rng(t)
+    x = g.standard_normal((n, c * t)).astype(np.float16)
+    w = dev(g.standard_normal((d, c, t)).astype(np.float16))
+    wp = scratch(eql.eqlinear_packed_weight_bytes(d, c, t, eql.EQL_F16))
+    eql.eqlinear_pack_weight(w, wp, d, c, t, eql.EQL_F16, eql.EQL_PACK_FWD)
+    nbytes = eql.eqlinear_bwd_w_workspace_bytes(n, c, d, t, eql.EQL_F16)
+    ws, y = scratch(nbytes), torch.empty((n, d * t), dtype=torch.float16, device=DEV)
+    eql.eqlinear_fwd_train(dev(x), wp, y, ws, nbytes, n, c, d, t, eql.EQL_F16)
+    section = (n // 16) * t * 2 * 64 * 16
+    units = ws.cpu().numpy()[section:2 * section].view(np.float16).reshape(n // 16, t, 2, 64, 8)
+    got = units[:, :, :, :c].transpose(1, 0, 2, 4, 3).reshape(t, n, c)
+    want = plain_spectrum_f16(x, t)
+    assert np.array_equal(got, want), "%d of %d values differ" % ((got != want).sum(), got.size)
