@@ -297,35 +297,37 @@ constexpr int64_t kSmallPartialBytes = 1 << 20;
 // Row ranges of a reduction over kgCount k-steps for `tiles` output items whose
 // partials take partBytesPerSplit bytes per range: enough ranges to give every compute
 // unit one item.
-// balance (the gradient from a checkpoint; the others keep the ranges, and so the bits, that
-// they had): where that leaves too few ranges, as many as balance a range's serial chain, about
-// kStepSeconds a k-step, against writing and adding one more set of partials at kPartialRate:
-// chain / S + S partials is least at S = sqrt(chain / partials).  Measured at T = 4, fp16, with
+// share (the gradient from a checkpoint with workspace to spare; the others keep the ranges, and so
+// the bits, that they had): where that leaves too few ranges, share / kShares of the way from there
+// to as many as balance a range's serial chain, about kStepSeconds a k-step, against writing and
+// adding one more set of partials at kPartialRate: chain / S + S partials is least at
+// S = sqrt(chain / partials).  Measured at T = 4, fp16, with
 // 1.3 / 1.6 / 2.6 / 5 us a step: 2000 rows of 256 x 256 channels 31.9 / 26.8 / 26.9 / 27.1 us,
 // 12608 rows of 96 x 384 channels 30.6 / 31.1 / 32.8 / 34.3 us.
+constexpr int kShares = 8;
 constexpr double kStepSeconds = 1.6e-6, kPartialRate = 1.5e12;
-int64_t split_count(int64_t tiles, int64_t kgCount, int64_t partBytesPerSplit, bool balance) {
+int64_t split_count(int64_t tiles, int64_t kgCount, int64_t partBytesPerSplit, int share) {
   const int64_t want = tiles >= kTargetWorkgroups ? 1 : kTargetWorkgroups / tiles;
   int64_t S = std::min<int64_t>(want, std::max<int64_t>(1, kgCount / kMinStepsPerSplit));
   if (S < want) {
     const int64_t S2 = std::min<int64_t>(want, std::max<int64_t>(1, kgCount / kMinStepsSmall));
     if (S2 * partBytesPerSplit <= kSmallPartialBytes) S = S2;
     const double best = std::sqrt((double)kgCount * kStepSeconds * kPartialRate / (double)std::max<int64_t>(1, partBytesPerSplit));
-    if (balance) S = std::max(S, std::min(S2, (int64_t)best));
+    S += std::max<int64_t>(0, std::min(S2, (int64_t)best) - S) * share / kShares;
   }
   return S;
 }
 
 // Row ranges (k-step ranges) of one GEMM launch.
-void plan_splits(GemmPlan& g, int64_t kgCount, int64_t partBytesPerSplit, bool balance) {
+void plan_splits(GemmPlan& g, int64_t kgCount, int64_t partBytesPerSplit, int share) {
   const int64_t tiles = g.groups * g.dTiles * g.cTiles;
   if (tiles == 0 || kgCount == 0) return;
-  const int64_t S = split_count(tiles, kgCount, partBytesPerSplit, balance);
+  const int64_t S = split_count(tiles, kgCount, partBytesPerSplit, share);
   g.kgPerSplit = ceil_div(kgCount, S);
   g.S = ceil_div(kgCount, g.kgPerSplit);
 }
 
-BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype, bool balance = false) {
+BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype, int share = 0) {
   BwdwPlan p;
   const int nr = n_real_planes(T), np = n_pairs(T);
   const int64_t wd = tile_width(Dp), wc = tile_width(Cp);
@@ -374,7 +376,7 @@ BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype, bool bal
     p.fCTiles = ceil_div(Cp, 32 * p.fNB);
     p.Cpad = p.fCTiles * 32 * p.fNB;
     const int64_t tiles = p.fDTiles * p.fCTiles;
-    const int64_t S = split_count(tiles, p.kgCount, (int64_t)T * Dp * Cp * (int64_t)sizeof(float), balance);
+    const int64_t S = split_count(tiles, p.kgCount, (int64_t)T * Dp * Cp * (int64_t)sizeof(float), share);
     p.fKgPerSplit = ceil_div(p.kgCount, S);
     p.fS = ceil_div(p.kgCount, p.fKgPerSplit);
     p.real.S = p.pair.S = p.fS;
@@ -383,8 +385,8 @@ BwdwPlan plan_bwdw(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype, bool bal
     p.partPBytes = (size_t)p.fS * (T - nr) * (size_t)Dp * (size_t)Cp * sizeof(float);
     return p;
   }
-  plan_splits(p.real, p.kgCount, (int64_t)nr * Dp * Cp * (int64_t)sizeof(float), balance);
-  plan_splits(p.pair, p.kgCount, (int64_t)(T - nr) * Dp * Cp * (int64_t)sizeof(float), balance);
+  plan_splits(p.real, p.kgCount, (int64_t)nr * Dp * Cp * (int64_t)sizeof(float), share);
+  plan_splits(p.pair, p.kgCount, (int64_t)(T - nr) * Dp * Cp * (int64_t)sizeof(float), share);
   p.dyhBytes = align256((size_t)p.kgCount * T * 2 * (size_t)p.Dpad * 16);
   p.xhBytes = align256((size_t)p.kgCount * T * 2 * (size_t)p.Cpad * 16);
   p.partRBytes = align256((size_t)p.real.S * nr * (size_t)Dp * (size_t)Cp * sizeof(float));
@@ -568,7 +570,9 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
   int st = check_sizes(N, Cp, Dp, T, dtype);
   if (st != EQL_OK) return st;
   if (view && (st = check_view(*view, N, dtype)) != EQL_OK) return st;
-  const BwdwPlan p = plan_bwdw(N, Cp, Dp, T, dtype, view != nullptr);
+  BwdwPlan p = plan_bwdw(N, Cp, Dp, T, dtype, view ? kShares : 0);
+  // As many of the further row ranges as the workspace holds.
+  for (int share = kShares; view && share-- > 0 && ws_bytes < p.total();) p = plan_bwdw(N, Cp, Dp, T, dtype, share);
   const bool needX = !spectra && !view, needDy = !spectra || p.fused;
   if (!dw || (N > 0 && ((needX && !x) || (needDy && !dy) || !workspace))) return EQL_EINVAL;
   if (ws_bytes < p.total()) return EQL_EINVAL;
@@ -835,7 +839,7 @@ int eqlinear_bwd_x(const void* dy, const void* w_packed_bwdx, void* dx, int64_t 
 
 size_t eqlinear_bwd_w_workspace_bytes(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
   if (check_sizes(N, Cp, Dp, T, dtype) != EQL_OK) return 0;
-  return std::max(plan_bwdw(N, Cp, Dp, T, dtype).total(), plan_bwdw(N, Cp, Dp, T, dtype, true).total());
+  return plan_bwdw(N, Cp, Dp, T, dtype).total();
 }
 
 int eqlinear_bwd_w(const void* x, const void* dy, void* dw, void* workspace, size_t ws_bytes,

@@ -468,7 +468,8 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
         def layer(g, w, ckpt, scale, shift, act, out, inp, need_w, need_x):
             """Input and weight gradient of one layer (inp -> out channels) for output gradient g.  At
             p4 fp16 the input gradient's kernel can leave g's spectrum for the weight gradient; elsewhere
-            that would be a launch of its own, which eqlinear_bwd_w_ckpt8 shares with the checkpoint's."""
+            that would be a launch of its own, which eqlinear_bwd_w_ckpt8 shares with the checkpoint's (and
+            with 32 MiB more, returned to the allocator after the call, it splits small layers further)."""
             dx = empty(N, inp * T) if need_x else None
             dw = torch.empty_like(w) if need_w else None
             n = eqlinear_bwd_w_workspace_bytes(N, inp, out, T, dt)
@@ -481,6 +482,7 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
             if need_x:
                 eqlinear_bwd_x(g, _packed(w, EQL_PACK_BWDX), dx, N, inp, out, T, dt)
             if need_w:
+                n += 32 << 20
                 eqlinear_bwd_w_ckpt8(ckpt, scale, shift, act, g, dw, scratch(n), n, N, inp, out, T, dt)
             return dx, dw
 

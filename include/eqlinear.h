@@ -239,8 +239,6 @@ int eqlinear_bwd_x(const void* dy, const void* w_packed_bwdx, void* dx, int64_t 
  * ties to the wider tile).  Both then hold fp32 partial spectra of the gradient:
  * whole Dp x Cp planes, one set per row range of the reduction over N (on the
  * separate path the real frequencies and the complex pairs are split separately).
- * The size also covers eqlinear_bwd_w_ckpt8 (eqlinear_block.h), which splits small
- * layers' rows further.
  */
 size_t eqlinear_bwd_w_workspace_bytes(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype);
 

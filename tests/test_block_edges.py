@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+import group_circulant_linear_p4_amd as eql
 from oracle import block_oracle as B
 
 
@@ -22,3 +23,19 @@ def test_checkpoint_of_the_largest_values(dtype, last):
     with np.errstate(over="raise"):
         back = B.unpack(codes, scale, 32).astype(np_type)
     assert (np.abs(back.astype(np.float64) - x) <= np.abs(x.astype(np.float64)).max(1, keepdims=True) / 127).all()
+
+
+def test_weight_gradient_workspace_is_the_plain_passes():
+    """A training step holds this many bytes from forward to backward, so it is what the plain passes
+    need and nothing for other entry points: spectra and one set of partial sums a row range."""
+    for args, nbytes in (((197, 128, 1024, 1, 0), 626688),
+                         ((1000, 1024, 512, 4, 1), 37552128),
+                         ((232, 22, 804, 4, 0), 520640),
+                         ((12608, 96, 384, 4, 1), 37404672),
+                         ((2000, 256, 256, 4, 1), 11436032),
+                         ((248, 1714, 592, 6, 0), 39589632),
+                         ((473, 717, 1391, 6, 1), 37207600),
+                         ((65536, 1024, 1024, 4, 1), 1207959552),
+                         ((16384, 64, 64, 8, 0), 79364096),
+                         ((1, 1, 1, 1, 0), 4352)):
+        assert eql.eqlinear_bwd_w_workspace_bytes(*args) == nbytes, args

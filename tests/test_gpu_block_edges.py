@@ -180,3 +180,24 @@ def test_fp16_spectra_are_rounded_once(t):
     got = units[:, :, :, :c].transpose(1, 0, 2, 4, 3).reshape(t, n, c)
     want = plain_spectrum_f16(x, t)
     assert np.array_equal(got, want), "%d of %d values differ" % ((got != want).sum(), got.size)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("shape", [(232, 22, 804, 4), (1000, 64, 300, 3), (197, 40, 500, 1), (60, 100, 90, 6), (900, 130, 70, 8)], ids=str)
+def test_weight_gradient_with_more_workspace(shape, dtype):
+    """More row ranges where the workspace holds their partial sums: the same gradient, and nothing
+    written past the bytes that were given."""
+    n, c, d, t = shape
+    g = np.random.default_rng(n + c)
+    codes, scale = B.pack(g.standard_normal((n, c * t)))
+    dy = g.standard_normal((n, d * t)).astype(NP[dtype])
+    ref = B.bwd_w(B.unpack(codes, scale, c * t), dy, t)
+    need, room = eql.eqlinear_bwd_w_workspace_bytes(n, c, d, t, DT[dtype]), 256
+    for more in (0, 256, 300000, 1 << 20, 32 << 20):
+        print("case", shape, dtype, more, flush=True)
+        ws = torch.full((need + more + room,), 85, dtype=torch.uint8, device=DEV)
+        dw = dev(np.zeros((d, c, t), NP[dtype]))
+        eql.eqlinear_bwd_w_ckpt8(dev(B.buffer(codes, scale)), None, None, eql.EQL_ACT_NONE, dev(dy), dw, ws, need + more, n, c, d, t, DT[dtype])
+        got = dw.cpu().numpy().astype(np.float64)
+        assert np.linalg.norm(got - ref) <= (1e-5 if dtype == "f32" else 3e-3) * np.linalg.norm(ref)
+        assert (ws[need + more:] == 85).all().item()
