@@ -506,6 +506,12 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
         return dx, dgamma, dbeta, dw1, db1, dw2, db2, None, None
 
 
+def _as_made(m, cls) -> bool:
+    """Calling m is cls.forward and nothing else: no subclass's or instance's forward, no hooks."""
+    return (isinstance(m, cls) and getattr(m.forward, "__func__", None) is cls.forward
+            and not (m._forward_hooks or m._forward_pre_hooks or m._backward_hooks or m._backward_pre_hooks))
+
+
 class EQMLPBlock(torch.nn.Module):
     """Pre-norm transformer MLP block, x + W2 gelu(W1 norm(x) + b1) + b2, over C_T: channels*T ->
     hidden_channels*T -> channels*T features.
@@ -513,7 +519,9 @@ class EQMLPBlock(torch.nn.Module):
     ckpt8 (the default) keeps the normalised rows and GELU's input in 8 bits for the backward:
     about C' + H' bytes per group element and row, against 2 C' + 4 H' in fp16 (4 C' + 8 H' in
     fp32) and as much again for the kept spectra when it is off; the gradients are those of the
-    rounded activations (each within 1/127 of its block's largest)."""
+    rounded activations (each within 1/127 of its block's largest).  The block then reads its
+    submodules' parameters; where a submodule was replaced, hooked or set to compute something else,
+    it calls them one after the other, as without ckpt8."""
 
     def __init__(self, channels: int, hidden_channels: int, group_order: int = 4, eps: float = 1e-5, device=None,
                  dtype=None, ckpt8: bool = True):
@@ -525,10 +533,18 @@ class EQMLPBlock(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         n, a, b = self.norm, self.fc1, self.fc2
-        if self.ckpt8:
+        if self.ckpt8 and self._as_made():
             return EQMLPBlock8bitFunction.apply(x, n.weight, n.bias, a.weight, a.bias, b.weight, b.bias, n.eps,
                                                 torch.is_grad_enabled())
         return b(a(n(x)), residual=x)
+
+    def _as_made(self) -> bool:
+        """The submodules compute norm, gelu(W1 . + b1) and W2 . + b2, and nothing runs around them."""
+        n, a, b = self.norm, self.fc1, self.fc2
+        return (_as_made(n, EQLayerNorm) and _as_made(a, EQLinear) and _as_made(b, EQLinear)
+                and a.activation == "gelu" and b.activation in (None, "none")
+                and all(p is not None for p in (n.weight, n.bias, a.bias, b.bias)) and n.group_order == a.weight.shape[2]
+                and not torch.nn.modules.module._has_any_global_hook())
 
     def extra_repr(self) -> str:
         return "ckpt8=%s" % self.ckpt8

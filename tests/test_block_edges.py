@@ -39,3 +39,33 @@ def test_weight_gradient_workspace_is_the_plain_passes():
                          ((16384, 64, 64, 8, 0), 79364096),
                          ((1, 1, 1, 1, 0), 4352)):
         assert eql.eqlinear_bwd_w_workspace_bytes(*args) == nbytes, args
+
+
+def test_block_sees_what_changed_in_its_submodules():
+    """Whether the 8-bit path's reading of the parameters stands for calling the submodules."""
+    import torch
+    from group_circulant_linear_p4_amd.layer import EQLayerNorm, EQLinear, EQMLPBlock
+
+    class Own(EQLinear):
+        def forward(self, x, residual=None):
+            return x
+
+    def change(f):
+        block = EQMLPBlock(3, 5, 4)
+        f(block)
+        return block._as_made()
+
+    assert change(lambda b: None)
+    assert change(lambda b: setattr(b, "fc1", EQLinear(3, 9, 4, bias=True, activation="gelu")))
+    assert change(lambda b: b.norm.__setattr__("eps", 1e-3)) and change(lambda b: setattr(b.fc2, "activation", "none"))
+    assert change(lambda b: b.fc1.register_forward_hook(print).remove())
+    for name in ("norm", "fc1", "fc2"):
+        for register in ("register_forward_hook", "register_forward_pre_hook", "register_full_backward_hook",
+                         "register_full_backward_pre_hook"):
+            assert not change(lambda b: getattr(getattr(b, name), register)(print)), (name, register)
+        assert not change(lambda b: setattr(getattr(b, name), "forward", print)), name
+        assert not change(lambda b: setattr(b, name, torch.nn.Identity())), name
+        assert not change(lambda b: setattr(getattr(b, name), "bias", None)), name
+    assert not change(lambda b: setattr(b, "fc2", Own(5, 3, 4, bias=True)))
+    assert not change(lambda b: setattr(b, "norm", EQLayerNorm(6, 2)))
+    assert not change(lambda b: setattr(b.fc1, "activation", None)) and not change(lambda b: setattr(b.fc2, "activation", "gelu"))
