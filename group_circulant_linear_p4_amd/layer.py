@@ -33,6 +33,17 @@ from . import (EQL_ACT_GELU, EQL_ACT_NONE, EQL_PACK_BWDX, EQL_PACK_FWD, eqlinear
                eqlinear_packed_weight_bytes)
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t, contiguous and on a 16-byte boundary (a slice of a larger tensor may start off one)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _rows(t: torch.Tensor, features: int) -> torch.Tensor:
+    """t as such rows."""
+    return _dense(t.reshape(-1, features))
+
+
 def _packed(w: torch.Tensor, mode: int) -> torch.Tensor:
     Dp, Cp, T = w.shape
     out_ch, in_ch = (Dp, Cp) if mode == EQL_PACK_FWD else (Cp, Dp)
@@ -51,8 +62,8 @@ class EQLinearFunction(torch.autograd.Function):
             raise ValueError("x has %d features, the weight expects C'*T = %d" % (x.shape[-1], Cp * T))
         if x.dtype != w.dtype:
             raise ValueError("x and w must share a dtype (fp16 or fp32)")
-        w = w.contiguous()
-        x2 = x.reshape(-1, Cp * T).contiguous()
+        w = _dense(w)
+        x2 = _rows(x, Cp * T)
         N = x2.shape[0]
         y = torch.empty((N, Dp * T), dtype=x.dtype, device=x.device)
         ws_bytes = eqlinear_bwd_w_workspace_bytes(N, Cp, Dp, T, x.dtype)
@@ -73,7 +84,7 @@ class EQLinearFunction(torch.autograd.Function):
         x2, w, ws = ctx.saved_tensors
         Dp, Cp, T = w.shape
         N = x2.shape[0]
-        dy2 = dy.reshape(-1, Dp * T).to(x2.dtype).contiguous()
+        dy2 = _rows(dy.to(x2.dtype), Dp * T)
         dx = dw = None
         need_dx, need_dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         train = ws is not None
@@ -136,12 +147,12 @@ class EQLinearFusedFunction(torch.autograd.Function):
             raise ValueError("bias must be on x's device (%s), got %s" % (x.device, b.device))
         if r is not None and r.device != x.device:
             raise ValueError("residual must be on x's device (%s), got %s" % (x.device, r.device))
-        w = w.contiguous()
-        x2 = x.reshape(-1, Cp * T).contiguous()
+        w = _dense(w)
+        x2 = _rows(x, Cp * T)
         N = x2.shape[0]
         if r is not None and r.numel() != N * Dp * T:
             raise ValueError("residual must have the output's shape")
-        r2 = r.reshape(N, Dp * T).contiguous() if r is not None else None
+        r2 = _rows(r, Dp * T) if r is not None else None
         y = torch.empty((N, Dp * T), dtype=x.dtype, device=x.device)
         # grad_mode is the caller's grad mode (autograd runs this body with grad disabled):
         # pre is kept only when a backward can follow.
@@ -168,7 +179,7 @@ class EQLinearFusedFunction(torch.autograd.Function):
         x2, w, pre, wsw = ctx.saved_tensors
         Dp, Cp, T = w.shape
         N = x2.shape[0]
-        dy2 = dy.reshape(-1, Dp * T).to(x2.dtype).contiguous()
+        dy2 = _rows(dy.to(x2.dtype), Dp * T)
         dr = dy2.reshape(ctx.res_shape) if ctx.res_shape is not None and ctx.needs_input_grad[3] else None
         dx = dw = db = None
         if not any(ctx.needs_input_grad[:3]):
@@ -260,8 +271,8 @@ class EQLinearP4MFunction(torch.autograd.Function):
         if x.dtype != w.dtype:
             raise ValueError("x and w must share a dtype (fp16 or fp32)")
         w4 = torch.empty((2 * Dp, 2 * Cp, 4), dtype=w.dtype, device=w.device)
-        eqlinear_p4m_expand_weight(w.contiguous(), w4, Dp, Cp, w.dtype)
-        x2 = x.reshape(-1, Cp * 8).contiguous()
+        eqlinear_p4m_expand_weight(_dense(w), w4, Dp, Cp, w.dtype)
+        x2 = _rows(x, Cp * 8)
         N = x2.shape[0]
         y = torch.empty((N, Dp * 8), dtype=x.dtype, device=x.device)
         ws_bytes = eqlinear_bwd_w_workspace_bytes(N, 2 * Cp, 2 * Dp, 4, x.dtype)
@@ -283,7 +294,7 @@ class EQLinearP4MFunction(torch.autograd.Function):
         x2, w4, ws = ctx.saved_tensors
         Dp, Cp = ctx.p4m_shape
         N = x2.shape[0]
-        dy2 = dy.reshape(-1, Dp * 8).to(x2.dtype).contiguous()
+        dy2 = _rows(dy.to(x2.dtype), Dp * 8)
         dx = dw = None
         need_dx, need_dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         train = ws is not None
@@ -329,12 +340,6 @@ class EQLinearP4M(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return "in_channels=%d, out_channels=%d, group=p4m" % (self.in_channels, self.out_channels)
-
-
-def _rows(t: torch.Tensor, features: int) -> torch.Tensor:
-    """t as contiguous rows on a 16-byte boundary (a slice of a larger tensor may start off one)."""
-    t = t.reshape(-1, features).contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 class EQLayerNormFunction(torch.autograd.Function):
@@ -436,7 +441,8 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
         if any(p.dtype != x.dtype or p.device != x.device for p in (gamma, beta, w1, b1, w2, b2)):
             raise ValueError("x and the block's parameters must share a dtype (fp16 or fp32) and a device")
         x2 = _rows(x, Cp * T)
-        gamma, beta, w1, b1, w2, b2 = (p.contiguous() for p in (gamma, beta, w1, b1, w2, b2))
+        gamma, beta, b1, b2 = (p.contiguous() for p in (gamma, beta, b1, b2))
+        w1, w2 = _dense(w1), _dense(w2)
         N, dt, dev = x2.shape[0], x.dtype, x.device
         train = grad_mode and any(ctx.needs_input_grad[:7])
         bytes8 = lambda c: torch.empty(eqlinear_ckpt8_bytes(N, c, T), dtype=torch.uint8, device=dev)  # noqa: E731

@@ -2,10 +2,11 @@
 import pytest
 import torch
 
-from group_circulant_linear_p4_amd.layer import EQLinear, EQMLPBlock
+from group_circulant_linear_p4_amd.layer import EQLinear, EQLinearP4M, EQMLPBlock
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+F16 = torch.float16
 
 
 def step(block, x, dy):
@@ -123,3 +124,57 @@ def test_block_runs_hooks_on_all_modules():
     finally:
         handle.remove()
     assert seen == ["EQLayerNorm", "EQLinear", "EQLinear", "EQMLPBlock"]
+
+
+def off_boundary(p):
+    """The parameter's values, two bytes past a 16-byte boundary."""
+    room = torch.empty(p.numel() + 1, dtype=p.dtype, device=p.device)
+    room[1:] = p.detach().reshape(-1)
+    return torch.nn.Parameter(room[1:].view(p.shape))
+
+
+LAYERS = {
+    "block": (15, lambda: EQMLPBlock(5, 7, 3, device=DEV, dtype=F16, ckpt8=True)),
+    "block whole": (15, lambda: EQMLPBlock(5, 7, 3, device=DEV, dtype=F16, ckpt8=False)),
+    "linear": (15, lambda: EQLinear(5, 7, 3, device=DEV, dtype=F16)),
+    "linear no spectra": (15, lambda: EQLinear(5, 7, 3, device=DEV, dtype=F16, keep_spectra=False)),
+    "linear fused": (15, lambda: EQLinear(5, 7, 3, bias=True, activation="gelu", device=DEV, dtype=F16)),
+    "p4m": (8, lambda: EQLinearP4M(1, 3, device=DEV, dtype=F16)),
+}
+
+
+@pytest.mark.parametrize("weights", ["as made", "off the boundary"])
+@pytest.mark.parametrize("name", list(LAYERS))
+def test_layers_take_any_contiguous_slice(name, weights):
+    """Rows from the second feature on of a flat tensor, weights likewise (as in a flattened parameter
+    buffer), and the gradient that torch.cat's backward hands out: as from aligned copies."""
+    features, make = LAYERS[name]
+    torch.manual_seed(4)
+    f = make()
+    flat = torch.randn(8 * features + 1, device=DEV, dtype=F16)
+    want = None
+    for aligned in (True, False):
+        x = flat[1:].view(8, features).detach()
+        x = (x.clone() if aligned else x).requires_grad_(True)
+        assert x.data_ptr() % 16 == (0 if aligned else 2)
+        if weights != "as made" and not aligned:
+            for m in f.modules():
+                for k, p in list(m.named_parameters(recurse=False)):
+                    setattr(m, k, off_boundary(p))
+        f.zero_grad()
+        y = f(x)
+        torch.manual_seed(9)
+        dy = torch.randn(1 + y.numel(), device=DEV, dtype=F16)
+        torch.cat([dy[:1], y.reshape(-1)]).backward(dy)
+        got = [y.detach(), x.grad] + [p.grad for p in f.parameters()]
+        if want is not None:
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+        want = [v.clone() for v in got]
+
+
+def test_fused_layer_takes_a_residual_off_the_boundary():
+    torch.manual_seed(5)
+    f = EQLinear(5, 5, 3, device=DEV, dtype=F16)
+    x, flat = torch.randn(8, 15, device=DEV, dtype=F16), torch.randn(8 * 15 + 1, device=DEV, dtype=F16)
+    r = flat[1:].view(8, 15)
+    assert torch.equal(f(x, r), f(x, r.clone()))
