@@ -14,13 +14,15 @@ GELU or a residual, the forward is eqlinear_fwd_fused (eqlinear_fwd_fused_train 
 weight needs a gradient) and the backward starts with eqlinear_fused_epilogue_bwd.  EQLayerNorm is the
 equivariant layer norm, and EQMLPBlock the pre-norm MLP block built from both, which by default
 keeps its activations for the backward in 8 bits (include/eqlinear_block.h).  Torch only allocates the buffers; every arithmetic step
-runs in the HIP library.
+runs in the HIP library.  The backward passes have no derivative of their own: asking for gradients
+of gradients raises.
 """
 from __future__ import annotations
 
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (EQL_ACT_GELU, EQL_ACT_NONE, EQL_PACK_BWDX, EQL_PACK_FWD, eqlinear_bwd_w,
                eqlinear_bwd_w_ckpt8, eqlinear_bwd_w_train, eqlinear_bwd_w_workspace_bytes, eqlinear_bwd_x,
@@ -80,6 +82,7 @@ class EQLinearFunction(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], Dp * T)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x2, w, ws = ctx.saved_tensors
         Dp, Cp, T = w.shape
@@ -175,6 +178,7 @@ class EQLinearFusedFunction(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], Dp * T)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x2, w, pre, wsw = ctx.saved_tensors
         Dp, Cp, T = w.shape
@@ -290,6 +294,7 @@ class EQLinearP4MFunction(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], Dp * 8)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x2, w4, ws = ctx.saved_tensors
         Dp, Cp = ctx.p4m_shape
@@ -377,6 +382,7 @@ class EQLayerNormFunction(torch.autograd.Function):
         return y.reshape(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x2, ckpt, mean, rstd, gamma = ctx.saved_tensors
         N, Cp, T = ctx.sizes
@@ -462,6 +468,7 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
         return y.reshape(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         h8, rstd, pre8, gamma, beta, w1, w2 = ctx.saved_tensors
         Hp, Cp, T = w1.shape

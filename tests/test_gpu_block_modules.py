@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from group_circulant_linear_p4_amd.layer import EQLinear, EQLinearP4M, EQMLPBlock
+from group_circulant_linear_p4_amd.layer import EQLayerNorm, EQLinear, EQLinearP4M, EQMLPBlock
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -178,3 +178,22 @@ def test_fused_layer_takes_a_residual_off_the_boundary():
     x, flat = torch.randn(8, 15, device=DEV, dtype=F16), torch.randn(8 * 15 + 1, device=DEV, dtype=F16)
     r = flat[1:].view(8, 15)
     assert torch.equal(f(x, r), f(x, r.clone()))
+
+
+@pytest.mark.parametrize("make", [lambda: EQLayerNorm(6, 4, device=DEV), lambda: EQLayerNorm(6, 4, device=DEV, ckpt8=True),
+                                  lambda: EQMLPBlock(6, 10, 4, device=DEV), lambda: EQMLPBlock(6, 10, 4, device=DEV, ckpt8=False),
+                                  lambda: EQLinear(6, 10, 4, device=DEV), lambda: EQLinear(6, 10, 4, bias=True, device=DEV),
+                                  lambda: EQLinearP4M(3, 5, device=DEV)],
+                         ids=["norm", "norm 8bit", "block 8bit", "block", "linear", "linear fused", "p4m"])
+def test_gradients_of_gradients_are_refused(make):
+    """The backward passes have no derivative of their own: asking for one raises, where a gradient
+    without a graph would count as a constant."""
+    torch.manual_seed(1)
+    f = make()
+    x = torch.randn(7, 24, device=DEV, requires_grad=True)
+    first, = torch.autograd.grad(f(x).square().sum(), x, create_graph=True)
+    plain, = torch.autograd.grad(f(x).square().sum(), x)
+    assert torch.equal(first.detach(), plain)
+    # Beside a term that has its second derivative, as a penalty on the gradient's norm would be.
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (first.square().sum() + x.square().sum()).backward()
