@@ -197,3 +197,42 @@ def test_gradients_of_gradients_are_refused(make):
     # Beside a term that has its second derivative, as a penalty on the gradient's norm would be.
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (first.square().sum() + x.square().sum()).backward()
+
+
+def along(fn, p, v, dy, eps):
+    """Central difference of sum(fn() dy) in p along v."""
+    with torch.no_grad():
+        p.add_(eps * v)
+        hi = (fn().double() * dy.double()).sum()
+        p.sub_(2 * eps * v)
+        lo = (fn().double() * dy.double()).sum()
+        p.add_(eps * v)
+    return ((hi - lo) / (2 * eps)).item()
+
+
+@pytest.mark.parametrize("ckpt8", [False, True])
+def test_block_gradients_along_their_own_direction(ckpt8):
+    """Along v = grad / |grad| the derivative is |grad| where the gradient is right (along a random
+    direction it is some |grad| / sqrt(size), less than what rounding to 8 bits may cost).  Central
+    differences with a step of 1e-2: the outputs' fp32 rounding, 2^-24 |y| an element, weighted by dy
+    and over twice the step, below 1e-3; the third derivative times step^2 / 6, below 1e-3 of |grad|:
+    1% of |grad|, which is 10 or more here, holds both.  8 bits: 4% more.  A gradient of zeros, one of
+    the other sign, one of half the size and a random one of the same length are all outside."""
+    torch.manual_seed(5)
+    block = EQMLPBlock(12, 20, 4, device=DEV, ckpt8=ckpt8)
+    with torch.no_grad():
+        block.norm.weight.add_(0.2 * torch.randn_like(block.norm.weight))
+        for p in (block.norm.bias, block.fc1.bias, block.fc2.bias):
+            p.add_(0.2 * torch.randn_like(p))
+    x = torch.randn(64, 48, device=DEV, requires_grad=True)
+    dy = torch.randn(64, 48, device=DEV)
+    block(x).backward(dy)
+    tol = 0.05 if ckpt8 else 0.01
+    for name, p in [("x", x), *block.named_parameters()]:
+        grad, rand = p.grad, torch.randn_like(p)
+        fits = []
+        for claim in (grad, torch.zeros_like(grad), -grad, 0.5 * grad, rand * (grad.norm() / rand.norm())):
+            v = grad / grad.norm()
+            diff = along(lambda: block(x), p, v, dy, 1e-2)
+            fits.append(abs(diff - (claim.double() * v.double()).sum().item()) <= tol * abs(diff))
+        assert fits == [True, False, False, False, False], (name, fits)
