@@ -10,8 +10,13 @@ namespace eql {
                 : (stream ? (const void*)&kernel<float, false, true> : (const void*)&kernel<float, false, false>)))
 
 hipError_t launch_ckpt_pack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s) {
+  // Rows that start inside a line are never streamed (load_chunk8).
   const bool whole = a.R % 8 == 0;
-  return launch_kernel(EQL_PICK(eql_ckpt_pack_kernel), grid, a, s);
+  const void* fn;
+  if (!whole) fn = f16 ? (const void*)&eql_ckpt_pack_kernel<_Float16, false, false> : (const void*)&eql_ckpt_pack_kernel<float, false, false>;
+  else if (stream) fn = f16 ? (const void*)&eql_ckpt_pack_kernel<_Float16, true, true> : (const void*)&eql_ckpt_pack_kernel<float, true, true>;
+  else fn = f16 ? (const void*)&eql_ckpt_pack_kernel<_Float16, true, false> : (const void*)&eql_ckpt_pack_kernel<float, true, false>;
+  return launch_kernel(fn, grid, a, s);
 }
 
 hipError_t launch_ckpt_unpack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s) {

@@ -3,15 +3,18 @@
 
 namespace eql {
 
+// The chunks a lane that norm_shape gives for LPR lanes (rows of up to kNormBwdMaxRow features).
 template <typename Elt, int LPR, bool WHOLE, bool STREAM, bool CKPT>
 static const void* bwd_k(int k) {
-  switch (k) {
-    case 1: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 1, WHOLE, STREAM, CKPT>;
-    case 2: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 2, WHOLE, STREAM, CKPT>;
-    case 3: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 3, WHOLE, STREAM, CKPT>;
-    case 4: return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 4, WHOLE, STREAM, CKPT>;
-    default: return nullptr;
+  if constexpr (LPR <= 64) {
+    if (k == 1) return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 1, WHOLE, STREAM, CKPT>;
   }
+  if (k == 2) return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 2, WHOLE, STREAM, CKPT>;
+  if constexpr (LPR >= 64) {
+    if (k == 3) return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 3, WHOLE, STREAM, CKPT>;
+    if (k == 4) return (const void*)&eql_norm_bwd_kernel<Elt, LPR, 4, WHOLE, STREAM, CKPT>;
+  }
+  return nullptr;
 }
 
 template <typename Elt, bool WHOLE, bool STREAM, bool CKPT>
@@ -20,10 +23,14 @@ static const void* bwd_shape(NormShape sh) {
                       : (sh.lpr == 64 ? bwd_k<Elt, 64, WHOLE, STREAM, CKPT>(sh.k) : bwd_k<Elt, 256, WHOLE, STREAM, CKPT>(sh.k));
 }
 
+// Of rows that start inside a line only the codes are streamed (load_chunk8).
 template <typename Elt, bool CKPT>
 static const void* bwd_fn(NormShape sh, bool whole, bool stream) {
-  return whole ? (stream ? bwd_shape<Elt, true, true, CKPT>(sh) : bwd_shape<Elt, true, false, CKPT>(sh))
-               : (stream ? bwd_shape<Elt, false, true, CKPT>(sh) : bwd_shape<Elt, false, false, CKPT>(sh));
+  if (whole) return stream ? bwd_shape<Elt, true, true, CKPT>(sh) : bwd_shape<Elt, true, false, CKPT>(sh);
+  if constexpr (CKPT) {
+    if (stream) return bwd_shape<Elt, false, true, CKPT>(sh);
+  }
+  return bwd_shape<Elt, false, false, CKPT>(sh);
 }
 
 hipError_t launch_norm_bwd(bool f16, bool stream, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s) {
