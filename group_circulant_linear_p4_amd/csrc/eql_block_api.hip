@@ -39,7 +39,7 @@ int64_t even_grid(int64_t turns, int64_t most) { return ceil_div(turns, ceil_div
 // in 1024; N = 12608, R = 384 takes 8.0 us in two turns and 9.5 in one.
 int64_t norm_fwd_grid(int64_t turns) { return even_grid(turns, std::clamp<int64_t>(turns / 2, 1024, 8192)); }
 // Backward: as few as keep the memory busy, since each leaves two sums a channel to add: N =
-// 65536, R = 4096 fp16 takes 298 us in 512 workgroups, 313 in 256 and 356 in 768; N = 16384, R =
+// 65536, R = 4096 fp16 takes 318 us in 512 workgroups, 359 in 256 and 373 in 768; N = 16384, R =
 // 512 fp32 25 us in 256 to 768.
 // One for up to three turns: it writes the parameters' gradients itself, which saves a launch
 // (14 rows of R = 56 fp16: 12.6 -> 10.7 us for both passes).

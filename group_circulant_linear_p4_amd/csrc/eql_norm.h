@@ -11,9 +11,9 @@
 // pass wrote (eql_ckpt8.h).
 //
 // All of it is bound by memory: one read of each operand, one write of each result.  Rows of up
-// to kNormMaxRow features are held in registers between the two uses (statistics, result): LPR
-// lanes take a row, K chunks of 8 features a lane, chunk j of the row on lane j % LPR.  The
-// variance is the mean square of the centred row, a second pass over registers.  Sums are fp32.
+// to kNormFwdMaxRow (backward kNormBwdMaxRow) features are held in registers between the two uses
+// (statistics, result): LPR lanes take a row, K chunks of 8 features a lane, chunk j of the row on
+// lane j % LPR.  The variance is the mean square of the centred row, a second pass over registers.  Sums are fp32.
 // A workgroup takes rows 256 / LPR at a time in a grid-stride loop, with gamma and beta, and in
 // the backward pass the column sums of dy h and dy, in registers for the whole loop.
 // Longer rows go through the kernels at the end of this file.

@@ -112,11 +112,13 @@ int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void
  *     x[n][c*T+t] = act(gamma[c] value + beta[c])
  * gamma, beta: [Cp] of `dtype`, or NULL (1, 0), aligned to the element; act: EQL_ACT_NONE or
  * EQL_ACT_GELU (any other value is EQL_EINVAL).  x is formed in fp32 and transformed; only its
- * spectrum is rounded to `dtype`.  The rest as eqlinear_bwd_w, with the same two paths and the
+ * spectrum is rounded to `dtype` (as dy's; fp16: 4e-4 of the gradient's norm off, where its own last
+ * rounding is 2e-4).  The rest as eqlinear_bwd_w, with the same two paths and the
  * same workspace (eqlinear_bwd_w_workspace_bytes) or a larger one: with more, a layer of few rows or
  * channels is split into more row ranges, each with partial sums of its own (232 rows, 22 x 804
  * channels, T = 4, fp32: 54 us with that many bytes, 20 with 3 MB more).  32 MiB more has been
- * enough for any size tried.  The order of the sum depends on the sizes and on ws_bytes, on nothing else.
+ * enough for any size tried.  The order of the sum depends on the sizes and on ws_bytes, on nothing
+ * else.
  */
 int eqlinear_bwd_w_ckpt8(const void* ckpt, const void* gamma, const void* beta, int act, const void* dy, void* dw,
                          void* workspace, size_t ws_bytes, int64_t N, int64_t Cp, int64_t Dp, int T, int dtype,
