@@ -8,8 +8,10 @@ hand-written HIP kernels for gfx950 behind the C ABI in include/eqlinear.h.
 
 include/eqlinear_block.h adds the operators around the layer in a transformer block: the
 equivariant layer norm and 8-bit activation checkpoints with the passes that read them.
+include/eqlinear_rmsnorm.h is the RMS norm with the residual's addition, and include/eqlinear_q8.h
+the layer's inference form in 8-bit integers.
 
-This module is the thin ctypes binding of both headers: one Python function per C
+This module is the thin ctypes binding of these headers: one Python function per C
 entry point, with the same name and argument order.  Buffers may be given as
 torch tensors on a ROCm device or as raw device addresses (int); `stream` as a
 torch.cuda.Stream, a raw hipStream_t (int) or None for torch's current stream.
@@ -35,6 +37,9 @@ __all__ = [
     "eqlinear_layernorm_fwd", "eqlinear_layernorm_bwd_workspace_bytes", "eqlinear_layernorm_bwd",
     "eqlinear_layernorm_bwd_ckpt8", "eqlinear_fused_epilogue_bwd_ckpt8", "eqlinear_bwd_w_ckpt8",
     "eqlinear_ckpt8_spectrum",
+    "eqlinear_rmsnorm_abi_version", "eqlinear_rmsnorm_fwd", "eqlinear_rmsnorm_bwd_workspace_bytes", "eqlinear_rmsnorm_bwd",
+    "eqlinear_q8_abi_version", "eqlinear_q8_rows_bytes", "eqlinear_q8_quantize", "eqlinear_q8_rmsnorm",
+    "eqlinear_q8_weight_bytes", "eqlinear_q8_pack_weight", "eqlinear_q8_fwd",
 ]
 
 EQL_F32, EQL_F16 = 0, 1
@@ -116,7 +121,18 @@ def lib() -> ctypes.CDLL:
                 ("eqlinear_layernorm_bwd_ckpt8", [vp] * 9 + [sz, i64, i64, i32, i32, vp], i32),
                 ("eqlinear_fused_epilogue_bwd_ckpt8", [vp] * 5 + [sz, i64, i64, i32, i32, vp], i32),
                 ("eqlinear_bwd_w_ckpt8", [vp, vp, vp, i32, vp, vp, vp, sz, i64, i64, i64, i32, i32, vp], i32),
-                ("eqlinear_ckpt8_spectrum", [vp, vp, vp, i32, vp, sz, i64, i64, i64, i32, i32, vp], i32)):
+                ("eqlinear_ckpt8_spectrum", [vp, vp, vp, i32, vp, sz, i64, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_rmsnorm_abi_version", [], i32),
+                ("eqlinear_rmsnorm_fwd", [vp] * 6 + [i64, i64, i32, f32, i32, vp], i32),
+                ("eqlinear_rmsnorm_bwd_workspace_bytes", [i64, i64, i32, i32], sz),
+                ("eqlinear_rmsnorm_bwd", [vp] * 8 + [sz, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_q8_abi_version", [], i32),
+                ("eqlinear_q8_rows_bytes", [i64, i64, i32], sz),
+                ("eqlinear_q8_quantize", [vp, vp, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_q8_rmsnorm", [vp] * 5 + [i64, i64, i32, f32, i32, vp], i32),
+                ("eqlinear_q8_weight_bytes", [i64, i64, i32], sz),
+                ("eqlinear_q8_pack_weight", [vp, vp, i64, i64, i32, i32, vp], i32),
+                ("eqlinear_q8_fwd", [vp] * 5 + [i64, i64, i64, i32, i32, i32, vp], i32)):
             getattr(L, name).argtypes, getattr(L, name).restype = args, res
         _lib = L
     return _lib
@@ -368,3 +384,64 @@ def eqlinear_ckpt8_spectrum(ckpt, gamma, beta, act: int, workspace, ws_bytes: in
     """That input's half spectrum into the weight-gradient workspace, as eqlinear_fwd_train leaves it."""
     _check(lib().eqlinear_ckpt8_spectrum(_ptr(ckpt), _ptr(gamma), _ptr(beta), int(act), _ptr(workspace), int(ws_bytes),
                                          N, Cp, Dp, T, _dtype(dtype), _stream(stream)), "eqlinear_ckpt8_spectrum")
+
+
+# include/eqlinear_rmsnorm.h: RMS norm with the residual's addition.
+def eqlinear_rmsnorm_abi_version() -> int:
+    return lib().eqlinear_rmsnorm_abi_version()
+
+
+def eqlinear_rmsnorm_fwd(x, residual, gamma, sum, y, rstd, N: int, Cp: int, T: int, eps: float, dtype,
+                         stream=None) -> None:
+    """residual / gamma / sum / rstd may be None; sum may be x or residual, y too (but not sum)."""
+    _check(lib().eqlinear_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum), _ptr(y), _ptr(rstd), N, Cp, T,
+                                      float(eps), _dtype(dtype), _stream(stream)), "eqlinear_rmsnorm_fwd")
+
+
+def eqlinear_rmsnorm_bwd_workspace_bytes(N: int, Cp: int, T: int, dtype) -> int:
+    return lib().eqlinear_rmsnorm_bwd_workspace_bytes(N, Cp, T, _dtype(dtype))
+
+
+def eqlinear_rmsnorm_bwd(dy, sum, rstd, gamma, dres, dx, dgamma, workspace, ws_bytes: int, N: int, Cp: int, T: int, dtype,
+                         stream=None) -> None:
+    """gamma / dres / dgamma may be None; dx may be dy or dres."""
+    _check(lib().eqlinear_rmsnorm_bwd(_ptr(dy), _ptr(sum), _ptr(rstd), _ptr(gamma), _ptr(dres), _ptr(dx), _ptr(dgamma),
+                                      _ptr(workspace), int(ws_bytes), N, Cp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_rmsnorm_bwd")
+
+
+# include/eqlinear_q8.h: the layer in 8-bit integers.
+def eqlinear_q8_abi_version() -> int:
+    return lib().eqlinear_q8_abi_version()
+
+
+def eqlinear_q8_rows_bytes(N: int, Cp: int, T: int) -> int:
+    return lib().eqlinear_q8_rows_bytes(N, Cp, T)
+
+
+def eqlinear_q8_quantize(x, rows8, N: int, Cp: int, T: int, dtype, stream=None) -> None:
+    """x [N][Cp*T] -> its 8-bit rows."""
+    _check(lib().eqlinear_q8_quantize(_ptr(x), _ptr(rows8), N, Cp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_q8_quantize")
+
+
+def eqlinear_q8_rmsnorm(x, residual, gamma, sum, rows8, N: int, Cp: int, T: int, eps: float, dtype, stream=None) -> None:
+    """eqlinear_rmsnorm_fwd with its output as 8-bit rows; residual / gamma / sum may be None."""
+    _check(lib().eqlinear_q8_rmsnorm(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum), _ptr(rows8), N, Cp, T, float(eps),
+                                     _dtype(dtype), _stream(stream)), "eqlinear_q8_rmsnorm")
+
+
+def eqlinear_q8_weight_bytes(Dp: int, Cp: int, T: int) -> int:
+    return lib().eqlinear_q8_weight_bytes(Dp, Cp, T)
+
+
+def eqlinear_q8_pack_weight(w, w8, Dp: int, Cp: int, T: int, dtype, stream=None) -> None:
+    """w [Dp][Cp][T] -> its 8-bit packing."""
+    _check(lib().eqlinear_q8_pack_weight(_ptr(w), _ptr(w8), Dp, Cp, T, _dtype(dtype), _stream(stream)),
+           "eqlinear_q8_pack_weight")
+
+
+def eqlinear_q8_fwd(rows8, w8, bias, residual, y, N: int, Cp: int, Dp: int, T: int, dtype, act: int, stream=None) -> None:
+    """The layer on 8-bit rows and weight; bias / residual may be None, residual may be y."""
+    _check(lib().eqlinear_q8_fwd(_ptr(rows8), _ptr(w8), _ptr(bias), _ptr(residual), _ptr(y), N, Cp, Dp, T, _dtype(dtype),
+                                 int(act), _stream(stream)), "eqlinear_q8_fwd")

@@ -48,6 +48,13 @@ SOURCES = [
     "eql_spec8_f32.hip",
     "eql_norm_fwd.hip",
     "eql_norm_bwd.hip",
+    "eql_rms.hip",
+    "eql_q8_api.hip",
+    "eql_q8_pack.hip",
+    "eql_q8_rows_f16.hip",
+    "eql_q8_rows_f32.hip",
+    "eql_q8_gemm_f16.hip",
+    "eql_q8_gemm_f32.hip",
 ]
 
 CFLAGS = [

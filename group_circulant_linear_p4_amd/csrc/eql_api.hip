@@ -693,6 +693,8 @@ int run_bwdw(const void* x, const void* dy, void* dw, void* workspace, size_t ws
 
 namespace eql::host {
 
+Twiddles twiddles(int T) { return make_twiddles(T); }
+
 int check_sizes(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) { return ::check_sizes(N, Cp, Dp, T, dtype); }
 
 void epilogue_rows(int64_t N, int64_t Dp, int T, int dtype, int64_t* rowsPerBlock, int64_t* rowBlocks, size_t* partBytes) {

@@ -1,9 +1,10 @@
-// Internal launch interface of the block operators (layer norm, 8-bit checkpoints): between
+// Internal launch interface of the block operators (layer norm, RMS norm, 8-bit checkpoints): between
 // eql_block_api.hip and the kernel instantiations, and what it shares with eql_api.hip.
 #pragma once
 
 #include "eql_launch.h"
 #include "eql_norm.h"
+#include "eql_rms.h"
 
 namespace eql {
 
@@ -33,10 +34,17 @@ hipError_t launch_norm_fwd(bool f16, bool stream, NormShape sh, const NormArgs& 
 hipError_t launch_norm_fwd_wide(bool f16, const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(bool f16, bool stream, NormShape sh, bool ckpt, const NormArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_norm_bwd_wide(bool f16, bool ckpt, const NormArgs& a, unsigned colGrid, hipStream_t s);
+hipError_t launch_rms_fwd(bool f16, bool stream, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s);
+hipError_t launch_rms_fwd_wide(bool f16, const NormArgs& a, hipStream_t s);
+hipError_t launch_rms_bwd(bool f16, bool stream, NormShape sh, const NormArgs& a, unsigned grid, hipStream_t s);
+hipError_t launch_rms_bwd_wide(bool f16, const NormArgs& a, unsigned colGrid, hipStream_t s);
 hipError_t launch_norm_param(bool f16, const NormParamArgs& a, hipStream_t s);
 
 // Shared host code of eql_api.hip.
 namespace host {
+
+// The group transform's coefficients.
+Twiddles twiddles(int T);
 
 // EQL_OK, or the status that the sizes deserve.
 int check_sizes(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype);

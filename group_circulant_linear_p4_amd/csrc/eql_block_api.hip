@@ -1,4 +1,4 @@
-// C ABI of the block operators (declared in include/eqlinear_block.h): argument checks, launch
+// C ABI of the block operators (include/eqlinear_block.h, include/eqlinear_rmsnorm.h): argument checks, launch
 // shapes and launches on the caller's stream.  Nothing here allocates device memory or
 // synchronises the host.
 #include <algorithm>
@@ -8,6 +8,7 @@
 
 #include "eql_block.h"
 #include "eqlinear_block.h"
+#include "eqlinear_rmsnorm.h"
 
 using namespace eql;
 
@@ -55,14 +56,15 @@ struct BwdPlan {
   size_t total() const { return rowBytes + partBytes; }
 };
 
-BwdPlan plan_norm_bwd(int64_t N, int64_t Cp, int T) {
+// kinds: column sums a feature (the layer norm's weight and bias, the RMS norm's weight).
+BwdPlan plan_norm_bwd(int64_t N, int64_t Cp, int T, int kinds) {
   BwdPlan p;
   if (N == 0) return p;
   const int64_t R = Cp * T;
   if (R <= kNormBwdMaxRow) {
     p.shape = norm_shape(ceil_div(R, 8));
     p.grid = norm_bwd_grid(ceil_div(N, 256 / p.shape.lpr));
-    p.partBytes = (size_t)p.grid * 2 * (size_t)Cp * sizeof(float);
+    p.partBytes = (size_t)p.grid * kinds * (size_t)Cp * sizeof(float);
     return p;
   }
   p.wide = true;
@@ -71,7 +73,7 @@ BwdPlan plan_norm_bwd(int64_t N, int64_t Cp, int T) {
   while (p.rowsPerBlock > 1 && ceil_div(N, p.rowsPerBlock) * p.colBlocks < 1024) p.rowsPerBlock /= 2;
   p.rowBlocks = ceil_div(N, p.rowsPerBlock);
   p.rowBytes = ((size_t)N * 2 * sizeof(float) + 255) / 256 * 256;
-  p.partBytes = (size_t)p.rowBlocks * 2 * (size_t)R * sizeof(float);
+  p.partBytes = (size_t)p.rowBlocks * kinds * (size_t)R * sizeof(float);
   return p;
 }
 
@@ -92,16 +94,20 @@ NormArgs norm_args(int64_t N, int64_t Cp, int T) {
   return a;
 }
 
-// Both backward entry points: ckpt null means x, mean and rstd.
-int norm_bwd(bool fromCkpt, const void* dy, const void* x, const void* ckpt, const float* mean, const float* rstd,
+// What a norm's backward pass reads beside dy: x and the layer norm's mean, its checkpoint, or x alone.
+enum class From { kMean, kCkpt, kRms };
+
+// The backward entry points of both norms.
+int norm_bwd(From from, const void* dy, const void* x, const void* ckpt, const float* mean, const float* rstd,
              const void* gamma, const void* dres, void* dx, void* dgamma, void* dbeta, void* workspace, size_t ws_bytes,
              int64_t N, int64_t Cp, int T, int dtype, void* stream) {
   const int st = host::check_sizes(N, Cp, 1, T, dtype);
   if (st != EQL_OK) return st;
-  const BwdPlan p = plan_norm_bwd(N, Cp, T);
+  const bool fromCkpt = from == From::kCkpt, rms = from == From::kRms;
+  const BwdPlan p = plan_norm_bwd(N, Cp, T, rms ? 1 : 2);
   const bool params = dgamma || dbeta;
   if (N > 0) {
-    if (!dy || !dx || !rstd || (fromCkpt ? !ckpt : (!x || !mean))) return EQL_EINVAL;
+    if (!dy || !dx || !rstd || (fromCkpt ? !ckpt : (!x || (!rms && !mean)))) return EQL_EINVAL;
     // The wide path keeps its row means in the workspace, the others only parameter sums.
     const size_t need = params ? p.total() : p.rowBytes;
     if (need && (!workspace || ws_bytes < need)) return EQL_EINVAL;
@@ -134,10 +140,13 @@ int norm_bwd(bool fromCkpt, const void* dy, const void* x, const void* ckpt, con
       a.rowSums = reinterpret_cast<float*>(ws);
       a.colBlocks = (int)p.colBlocks;
       a.rowsPerBlock = (int)p.rowsPerBlock;
-      e = launch_norm_bwd_wide(f16, fromCkpt, a, (unsigned)(p.rowBlocks * p.colBlocks), s);
+      const unsigned grid = (unsigned)(p.rowBlocks * p.colBlocks);
+      e = rms ? launch_rms_bwd_wide(f16, a, grid, s) : launch_norm_bwd_wide(f16, fromCkpt, a, grid, s);
     } else {
       const int64_t moved = elt_bytes(dtype) * (2 + (dres ? 1 : 0)) + (fromCkpt ? 1 : elt_bytes(dtype));
-      e = launch_norm_bwd(f16, streams(N * (int64_t)a.R * moved), p.shape, fromCkpt, a, (unsigned)p.grid, s);
+      const bool stream_in = streams(N * (int64_t)a.R * moved);
+      e = rms ? launch_rms_bwd(f16, stream_in, p.shape, a, (unsigned)p.grid, s)
+              : launch_norm_bwd(f16, stream_in, p.shape, fromCkpt, a, (unsigned)p.grid, s);
     }
     if (e != hipSuccess) return EQL_EHIP;
     if (direct) return EQL_OK;
@@ -151,7 +160,7 @@ int norm_bwd(bool fromCkpt, const void* dy, const void* x, const void* ckpt, con
   q.C = (int)Cp;
   q.F = p.wide ? T : 1;
   q.groups = (int)ceil_div(Cp, 16);
-  q.blockStride = 2 * Cp * q.F;
+  q.blockStride = (rms ? 1 : 2) * Cp * q.F;
   return status_of(launch_norm_param(f16, q, s));
 }
 
@@ -183,6 +192,8 @@ int ckpt_copy(bool pack, const void* x, const void* ckpt, int64_t N, int64_t Cp,
 extern "C" {
 
 int eqlinear_block_abi_version(void) { return 100; }
+
+int eqlinear_rmsnorm_abi_version(void) { return 100; }
 
 size_t eqlinear_ckpt8_bytes(int64_t N, int64_t Cp, int T) {
   if (host::check_sizes(N, Cp, 1, T, EQL_F16) != EQL_OK) return 0;
@@ -231,21 +242,63 @@ int eqlinear_layernorm_fwd(const void* x, const void* gamma, const void* beta, v
 
 size_t eqlinear_layernorm_bwd_workspace_bytes(int64_t N, int64_t Cp, int T, int dtype) {
   if (host::check_sizes(N, Cp, 1, T, dtype) != EQL_OK) return 0;
-  return plan_norm_bwd(N, Cp, T).total();
+  return plan_norm_bwd(N, Cp, T, 2).total();
 }
 
 int eqlinear_layernorm_bwd(const void* dy, const void* x, const float* mean, const float* rstd, const void* gamma,
                            const void* dres, void* dx, void* dgamma, void* dbeta, void* workspace, size_t ws_bytes,
                            int64_t N, int64_t Cp, int T, int dtype, void* stream) {
-  return norm_bwd(false, dy, x, nullptr, mean, rstd, gamma, dres, dx, dgamma, dbeta, workspace, ws_bytes, N, Cp, T,
+  return norm_bwd(From::kMean, dy, x, nullptr, mean, rstd, gamma, dres, dx, dgamma, dbeta, workspace, ws_bytes, N, Cp, T,
                   dtype, stream);
 }
 
 int eqlinear_layernorm_bwd_ckpt8(const void* dy, const void* ckpt, const float* rstd, const void* gamma,
                                  const void* dres, void* dx, void* dgamma, void* dbeta, void* workspace,
                                  size_t ws_bytes, int64_t N, int64_t Cp, int T, int dtype, void* stream) {
-  return norm_bwd(true, dy, nullptr, ckpt, nullptr, rstd, gamma, dres, dx, dgamma, dbeta, workspace, ws_bytes, N, Cp, T,
+  return norm_bwd(From::kCkpt, dy, nullptr, ckpt, nullptr, rstd, gamma, dres, dx, dgamma, dbeta, workspace, ws_bytes, N, Cp, T,
                   dtype, stream);
+}
+
+int eqlinear_rmsnorm_fwd(const void* x, const void* residual, const void* gamma, void* sum, void* y, float* rstd, int64_t N,
+                         int64_t Cp, int T, float eps, int dtype, void* stream) {
+  const int st = host::check_sizes(N, Cp, 1, T, dtype);
+  if (st != EQL_OK) return st;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return EQL_EINVAL;
+  if (N == 0) return EQL_OK;
+  if (!x || !y || sum == y) return EQL_EINVAL;
+  if (off(x, 16) || off(residual, 16) || off(sum, 16) || off(y, 16) || off(rstd, 4) || off(gamma, (uintptr_t)elt_bytes(dtype)))
+    return EQL_EALIGN;
+  NormArgs a = norm_args(N, Cp, T);
+  a.x = x;
+  a.res = residual;
+  a.gamma = gamma;
+  a.sum = sum;
+  a.y = y;
+  a.rstd = rstd;
+  a.eps = eps;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool f16 = dtype == EQL_F16;
+  if (a.R > kNormFwdMaxRow) {
+    if (N > kMaxGrid / 4) return EQL_EINVAL;
+    return status_of(launch_rms_fwd_wide(f16, a, s));
+  }
+  const NormShape sh = norm_shape(a.pitch / 8);
+  a.table = norm_table(sh.lpr, a.R, T, elt_bytes(dtype), 1);
+  const int64_t grid = norm_fwd_grid(ceil_div(N, 256 / sh.lpr));
+  const int64_t moved = elt_bytes(dtype) * (2 + (residual ? 1 : 0) + (sum ? 1 : 0));
+  return status_of(launch_rms_fwd(f16, streams(N * (int64_t)a.R * moved), sh, a, (unsigned)grid, s));
+}
+
+size_t eqlinear_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t Cp, int T, int dtype) {
+  if (host::check_sizes(N, Cp, 1, T, dtype) != EQL_OK) return 0;
+  return plan_norm_bwd(N, Cp, T, 1).total();
+}
+
+int eqlinear_rmsnorm_bwd(const void* dy, const void* sum, const float* rstd, const void* gamma, const void* dres, void* dx,
+                         void* dgamma, void* workspace, size_t ws_bytes, int64_t N, int64_t Cp, int T, int dtype,
+                         void* stream) {
+  return norm_bwd(From::kRms, dy, sum, nullptr, nullptr, rstd, gamma, dres, dx, dgamma, nullptr, workspace, ws_bytes, N, Cp,
+                  T, dtype, stream);
 }
 
 int eqlinear_fused_epilogue_bwd_ckpt8(const void* dy, const void* pre_ckpt, void* dpre, void* dbias, void* workspace,

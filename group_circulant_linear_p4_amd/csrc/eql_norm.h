@@ -45,6 +45,8 @@ struct NormArgs {
   int table;          // 1: parameters spread through LDS (norm_table)
   float eps, invR;
   int rowsPerBlock, colBlocks;  // wide backward
+  const void* res;    // RMS norm forward: added to x, or null
+  void* sum;          // RMS norm forward: receives x + res, or null (may be x or res)
 };
 
 // Sum over the LPR lanes of a row (LPR <= 64), on every lane.
@@ -298,9 +300,11 @@ __device__ __forceinline__ float group_sum(float v) {
 // wave, or one in all where a row takes the whole workgroup.
 __host__ __device__ constexpr int norm_bwd_copies(int lpr) { return lpr > 64 ? 1 : 4; }
 
-// CKPT: h from the checkpoint (codes, scales, rstd), else from x, mean and rstd.
+// CKPT: h from the checkpoint (codes, scales, rstd), else from x, mean and rstd.  RMS: the RMS norm's
+// backward, which is this without the mean of x, the mean of g and the bias; its blocks of column
+// sums are [C].
 // Dynamic LDS: norm_bwd_copies(LPR) * R floats, for the column sums at the end, or the table.
-template <typename Elt, int LPR, int K, bool WHOLE, bool STREAM, bool CKPT>
+template <typename Elt, int LPR, int K, bool WHOLE, bool STREAM, bool CKPT, bool RMS = false>
 __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   using V = typename Chunk<Elt>::V;
   constexpr int G = 256 / LPR;
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   auto load = [&](int64_t row) __attribute__((always_inline)) {
     const bool live = row < a.N;
     rstdN = live ? a.rstd[row] : 0.0f;
-    if constexpr (!CKPT) meanN = live ? a.mean[row] : 0.0f;
+    if constexpr (!CKPT && !RMS) meanN = live ? a.mean[row] : 0.0f;
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int f0 = (lane + i * LPR) * 8;
@@ -362,7 +366,8 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
     const float rstd = rstdN;
     float h[K][8];
     V dy[K], r[K];
-    float s[2] = {0.0f, 0.0f};
+    constexpr int SUMS = RMS ? 1 : 2;
+    float s[SUMS] = {};
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       dy[i] = dyN[i];
@@ -371,9 +376,9 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
         decode8(wN[i], scale_step(scN[i]), h[i]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = ((float)xN[i][e] - meanN) * rstd;
+        for (int e = 0; e < 8; ++e) h[i][e] = (RMS ? (float)xN[i][e] : (float)xN[i][e] - meanN) * rstd;
         int n = a.R - (lane + i * LPR) * 8;
-        if (a.R < (i + 1) * LPR * 8) {
+        if (!RMS && a.R < (i + 1) * LPR * 8) {
           // Missing features count as zero: mean rstd may overflow where no h does.
           asm volatile("" : "+v"(n));
 #pragma unroll
@@ -389,14 +394,16 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
         // Past the row's end dy and h are zero.
         const float d = (float)dy[i][e];
         const float g = d * (float)gam[i][e];
-        s[0] += g;
-        s[1] = __builtin_fmaf(g, h[i][e], s[1]);
-        sb[i][e] += d;
+        if constexpr (!RMS) {
+          s[0] += g;
+          sb[i][e] += d;
+        }
+        s[SUMS - 1] = __builtin_fmaf(g, h[i][e], s[SUMS - 1]);
         sg[i][e] = __builtin_fmaf(d, h[i][e], sg[i][e]);
       }
     row_sums<LPR>(s, red[turn]);
     turn ^= 1;
-    const float m1 = row_mean(a, s[0]), m2 = row_mean(a, s[1]);
+    const float m1 = RMS ? 0.0f : row_mean(a, s[0]), m2 = row_mean(a, s[SUMS - 1]);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int f0 = (lane + i * LPR) * 8;
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float g = (float)dy[i][e] * (float)gam[i][e];
-        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, g - m1), (float)r[i][e]);
+        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[i][e], m2, RMS ? g : g - m1), (float)r[i][e]);
       }
       store_chunk8<Elt, WHOLE>(static_cast<Elt*>(a.dx) + row * a.R + f0, live ? a.R - f0 : 0, o);
     }
@@ -415,9 +422,10 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_kernel(const NormArgs a) {
   constexpr int COPIES = norm_bwd_copies(LPR);
   const int copy = LPR > 64 ? 0 : (int)threadIdx.x >> 6;
   const bool writes = LPR >= 64 || (threadIdx.x & 63) < LPR;
-  float* out = a.part + (int64_t)blockIdx.x * 2 * a.C;
+  constexpr int KINDS = RMS ? 1 : 2;
+  float* out = a.part + (int64_t)blockIdx.x * KINDS * a.C;
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
+  for (int which = 0; which < KINDS; ++which) {
     void* direct = which ? a.dbeta : a.dgamma;
     __syncthreads();
 #pragma unroll
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(1024) eql_norm_fwd_wide_kernel(const NormArgs 
 }
 
 // h of one chunk, from x or the checkpoint (zero past the row's end).
-template <typename Elt, bool CKPT>
+template <typename Elt, bool CKPT, bool RMS>
 __device__ __forceinline__ void wide_h(const NormArgs& a, int64_t row, int f0, int n, float mean, float rstd, float (&h)[8]) {
   if constexpr (CKPT) {
     const float step = scale_step(a.scales[row * (a.pitch / kCkptBlock) + f0 / kCkptBlock]);
@@ -569,22 +577,22 @@ __device__ __forceinline__ void wide_h(const NormArgs& a, int64_t row, int f0, i
   } else {
     const auto u = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.x) + row * a.R + f0, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = e < n ? ((float)u[e] - mean) * rstd : 0.0f;
+    for (int e = 0; e < 8; ++e) h[e] = RMS ? (float)u[e] * rstd : (e < n ? ((float)u[e] - mean) * rstd : 0.0f);
   }
 }
 
-template <typename Elt, bool CKPT>
+template <typename Elt, bool CKPT, bool RMS = false>
 __global__ void __launch_bounds__(1024) eql_norm_bwd_rows_kernel(const NormArgs a) {
   __shared__ float red[32];
   const int64_t row = blockIdx.x;
-  const float rstd = a.rstd[row], mean = CKPT ? 0.0f : a.mean[row];
+  const float rstd = a.rstd[row], mean = CKPT || RMS ? 0.0f : a.mean[row];
   float s[2] = {0.0f, 0.0f};
   for (int f0 = (int)threadIdx.x * 8; f0 < a.R; f0 += 8192) {
     const int n = a.R - f0;
     const auto d = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
     const auto gam = spread<Elt>(a, a.gamma, f0, 1.0f);
     float h[8];
-    wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
+    wide_h<Elt, CKPT, RMS>(a, row, f0, n, mean, rstd, h);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float g = (float)d[e] * (float)gam[e];
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(1024) eql_norm_bwd_rows_kernel(const NormArgs 
 }
 
 // Workgroup: 256 chunks across (one a lane), rowsPerBlock rows down.
-template <typename Elt, bool CKPT>
+template <typename Elt, bool CKPT, bool RMS = false>
 __global__ void __launch_bounds__(256) eql_norm_bwd_cols_kernel(const NormArgs a) {
   const int cb = (int)blockIdx.x % a.colBlocks, rb = (int)blockIdx.x / a.colBlocks;
   const int f0 = (cb * 256 + (int)threadIdx.x) * 8;
@@ -609,26 +617,26 @@ __global__ void __launch_bounds__(256) eql_norm_bwd_cols_kernel(const NormArgs a
   for (int e = 0; e < 8; ++e) sg[e] = sb[e] = 0.0f;
   const int64_t r0 = (int64_t)rb * a.rowsPerBlock, r1 = min(a.N, r0 + a.rowsPerBlock);
   for (int64_t row = r0; row < r1; ++row) {
-    const float rstd = a.rstd[row], mean = CKPT ? 0.0f : a.mean[row];
-    const float m1 = a.rowSums[row * 2], m2 = a.rowSums[row * 2 + 1];
+    const float rstd = a.rstd[row], mean = CKPT || RMS ? 0.0f : a.mean[row];
+    const float m1 = RMS ? 0.0f : a.rowSums[row * 2], m2 = a.rowSums[row * 2 + 1];
     const auto d = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dy) + row * a.R + f0, n);
     auto r = zero_chunk<Elt>();
     if (a.dres) r = load_chunk8<Elt, false, false>(static_cast<const Elt*>(a.dres) + row * a.R + f0, n);
     float h[8], o[8];
-    wide_h<Elt, CKPT>(a, row, f0, n, mean, rstd, h);
+    wide_h<Elt, CKPT, RMS>(a, row, f0, n, mean, rstd, h);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float dv = (float)d[e], g = dv * (float)gam[e];
       sb[e] += dv;
       sg[e] = __builtin_fmaf(dv, h[e], sg[e]);
-      o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[e], m2, g - m1), (float)r[e]);
+      o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-h[e], m2, RMS ? g : g - m1), (float)r[e]);
     }
     store_chunk8<Elt, false>(static_cast<Elt*>(a.dx) + row * a.R + f0, n, o);
   }
   if (a.part) {
-    float* out = a.part + (int64_t)rb * 2 * a.R + f0;
+    float* out = a.part + (int64_t)rb * (RMS ? 1 : 2) * a.R + f0;
     store_chunk8<float, false>(out, n, sg);
-    store_chunk8<float, false>(out + a.R, n, sb);
+    if constexpr (!RMS) store_chunk8<float, false>(out + a.R, n, sb);
   }
 }
 

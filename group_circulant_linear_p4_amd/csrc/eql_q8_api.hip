@@ -1,0 +1,139 @@
+// C ABI of the layer in 8-bit integers (declared in include/eqlinear_q8.h): argument checks, launch
+// shapes and launches on the caller's stream.  Nothing here allocates device memory or synchronises
+// the host.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "eql_q8_launch.h"
+#include "eqlinear_q8.h"
+
+using namespace eql;
+
+namespace {
+
+constexpr int64_t kMaxGrid = (1LL << 24) - 1;  // workgroups of 256 threads per launch
+constexpr int64_t kMaxC = 65536;               // channels whose products' sums fit 32 bits
+
+int elt_bytes(int dtype) { return dtype == EQL_F16 ? 2 : 4; }
+bool off(const void* p, uintptr_t to) { return p && reinterpret_cast<uintptr_t>(p) % to != 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int status_of(hipError_t e) { return e == hipSuccess ? EQL_OK : EQL_EHIP; }
+
+int check(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
+  const int st = host::check_sizes(N, Cp, Dp, T, dtype);
+  if (st != EQL_OK) return st;
+  return Cp > kMaxC ? EQL_EUNSUPPORTED : EQL_OK;
+}
+
+size_t row_codes(int64_t N, int64_t Cp, int T) { return (size_t)N * (size_t)T * (size_t)q8_pitch(Cp); }
+size_t weight_codes(int64_t Dp, int64_t Cp, int T) { return (size_t)(q8_out(Dp) / 32 * q8_blocks(Cp)) * (size_t)T * 2048; }
+
+// Both entry points that write rows.
+int write_rows(bool norm, const void* x, const void* res, const void* gamma, void* sum, void* rows8, int64_t N, int64_t Cp,
+               int T, float eps, int dtype, void* stream) {
+  const int st = check(N, Cp, 1, T, dtype);
+  if (st != EQL_OK) return st;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return EQL_EINVAL;
+  if (N == 0) return EQL_OK;
+  if (!x || !rows8) return EQL_EINVAL;
+  if (off(x, 16) || off(res, 16) || off(sum, 16) || off(rows8, 16) || off(gamma, (uintptr_t)elt_bytes(dtype))) return EQL_EALIGN;
+  Q8RowsArgs a{};
+  a.x = x;
+  a.res = res;
+  a.gamma = gamma;
+  a.sum = sum;
+  a.codes = static_cast<unsigned char*>(rows8);
+  a.scales = reinterpret_cast<float*>(a.codes + row_codes(N, Cp, T));
+  a.N = N;
+  a.C = (int)Cp;
+  a.pitch = (int)q8_pitch(Cp);
+  a.norm = norm;
+  a.eps = eps;
+  a.invR = (float)(1.0 / (double)(Cp * T));
+  a.tw = host::twiddles(T);
+  const NormShape sh = q8_shape(ceil_div(Cp, q8_chunk(T)), T);
+  int64_t grid = N;
+  if (sh.k) grid = std::min(ceil_div(N, 256 / sh.lpr), kMaxGrid);
+  else if (N > kMaxGrid) return EQL_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return status_of(dtype == EQL_F16 ? launch_q8_rows_f16(T, sh, a, (unsigned)grid, s) : launch_q8_rows_f32(T, sh, a, (unsigned)grid, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+int eqlinear_q8_abi_version(void) { return 100; }
+
+size_t eqlinear_q8_rows_bytes(int64_t N, int64_t Cp, int T) {
+  if (check(N, Cp, 1, T, EQL_F16) != EQL_OK) return 0;
+  return row_codes(N, Cp, T) + (size_t)N * n_freqs(T) * sizeof(float);
+}
+
+size_t eqlinear_q8_weight_bytes(int64_t Dp, int64_t Cp, int T) {
+  if (check(0, Cp, Dp, T, EQL_F16) != EQL_OK) return 0;
+  return weight_codes(Dp, Cp, T) + (size_t)q8_out(Dp) * n_freqs(T) * sizeof(float);
+}
+
+int eqlinear_q8_pack_weight(const void* w, void* w8, int64_t Dp, int64_t Cp, int T, int dtype, void* stream) {
+  const int st = check(0, Cp, Dp, T, dtype);
+  if (st != EQL_OK) return st;
+  if (!w || !w8) return EQL_EINVAL;
+  if (off(w, 16) || off(w8, 16)) return EQL_EALIGN;
+  Q8PackArgs a{};
+  a.w = w;
+  a.codes = static_cast<unsigned char*>(w8);
+  a.scales = reinterpret_cast<float*>(a.codes + weight_codes(Dp, Cp, T));
+  a.D = (int)Dp;
+  a.C = (int)Cp;
+  a.Dpad = (int)q8_out(Dp);
+  a.kblocks = (int)q8_blocks(Cp);
+  a.tw = host::twiddles(T);
+  return status_of(launch_q8_pack(dtype == EQL_F16, T, a, static_cast<hipStream_t>(stream)));
+}
+
+int eqlinear_q8_quantize(const void* x, void* rows8, int64_t N, int64_t Cp, int T, int dtype, void* stream) {
+  return write_rows(false, x, nullptr, nullptr, nullptr, rows8, N, Cp, T, 0.0f, dtype, stream);
+}
+
+int eqlinear_q8_rmsnorm(const void* x, const void* residual, const void* gamma, void* sum, void* rows8, int64_t N,
+                        int64_t Cp, int T, float eps, int dtype, void* stream) {
+  return write_rows(true, x, residual, gamma, sum, rows8, N, Cp, T, eps, dtype, stream);
+}
+
+int eqlinear_q8_fwd(const void* rows8, const void* w8, const void* bias, const void* residual, void* y, int64_t N,
+                    int64_t Cp, int64_t Dp, int T, int dtype, int act, void* stream) {
+  const int st = check(N, Cp, Dp, T, dtype);
+  if (st != EQL_OK) return st;
+  if (act != EQL_ACT_NONE && act != EQL_ACT_GELU) return EQL_EINVAL;
+  if (N == 0) return EQL_OK;
+  if (!rows8 || !w8 || !y) return EQL_EINVAL;
+  if (off(rows8, 16) || off(w8, 16) || off(y, 16) || off(residual, 16) || off(bias, (uintptr_t)elt_bytes(dtype))) return EQL_EALIGN;
+  Q8FwdArgs a{};
+  a.f.y = y;
+  a.f.N = (int)N;
+  a.f.Dout = (int)Dp;
+  a.f.tw = host::twiddles(T);
+  a.f.bias = bias;
+  a.f.res = residual;
+  a.f.act = act;
+  a.codes = static_cast<const unsigned char*>(rows8);
+  a.rowScales = reinterpret_cast<const float*>(a.codes + row_codes(N, Cp, T));
+  a.w = static_cast<const unsigned char*>(w8);
+  a.wScales = reinterpret_cast<const float*>(a.w + weight_codes(Dp, Cp, T));
+  a.pitch = (int)q8_pitch(Cp);
+  a.kblocks = (int)q8_blocks(Cp);
+  a.Dpad = (int)q8_out(Dp);
+  const int64_t bm = 32 * q8_mb(T), bn = 128 * q8_nb(T);
+  const bool large = ceil_div(N, bm) * ceil_div(Dp, bn) >= 128;
+  const int64_t rowTiles = ceil_div(N, large ? bm : 32), colTiles = ceil_div(Dp, large ? bn : 32);
+  if (rowTiles * colTiles > kMaxGrid / 2) return EQL_EINVAL;
+  a.rowTiles = (int)rowTiles;
+  a.colTiles = (int)colTiles;
+  const unsigned grid = (unsigned)(rowTiles * colTiles);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return status_of(dtype == EQL_F16 ? launch_q8_fwd_f16(T, large, a, grid, s) : launch_q8_fwd_f32(T, large, a, grid, s));
+}
+
+}  // extern "C"

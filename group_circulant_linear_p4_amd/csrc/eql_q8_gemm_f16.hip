@@ -1,0 +1,10 @@
+// Instantiations of the 8-bit product kernels: f16 outputs.
+#include "eql_q8_gemm_inst.h"
+
+namespace eql {
+
+hipError_t launch_q8_fwd_f16(int T, bool large, const Q8FwdArgs& a, unsigned grid, hipStream_t s) {
+  return q8_fwd_launch<_Float16>(T, large, a, grid, s);
+}
+
+}  // namespace eql

@@ -1,0 +1,10 @@
+// Instantiations of the 8-bit row kernels: f16.
+#include "eql_q8_rows_inst.h"
+
+namespace eql {
+
+hipError_t launch_q8_rows_f16(int T, NormShape sh, const Q8RowsArgs& a, unsigned grid, hipStream_t s) {
+  return q8_rows_launch<_Float16>(T, sh, a, grid, s);
+}
+
+}  // namespace eql
