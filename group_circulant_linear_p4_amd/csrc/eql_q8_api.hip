@@ -29,6 +29,20 @@ int check(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
 size_t row_codes(int64_t N, int64_t Cp, int T) { return (size_t)N * (size_t)T * (size_t)q8_pitch(Cp); }
 size_t weight_codes(int64_t Dp, int64_t Cp, int T) { return (size_t)(q8_out(Dp) / 32 * q8_blocks(Cp)) * (size_t)T * 2048; }
 
+// Which kernel a product takes.  The big tile reads the operands least, once it has a tile for most compute units
+// (p4 fp16 with residual, 65536 rows of 256 -> 1024 channels: 275 us against the medium tile's 322; 12608 rows of 384
+// -> 96, 197 tiles: 10.8 and 11.9; 1000 rows of 384 -> 384, 48 tiles: 9.1 and 7.0).  The small kernel splits the input
+// channels instead, where few medium tiles would each walk many of them (32 rows of 1024 -> 1024, 8 tiles: 5.9 us and
+// 10.6; 300 rows, 80 tiles: 13.7 and 12.1).
+Q8Kind product_kind(int64_t N, int64_t Cp, int64_t Dp, int T) {
+  if (N <= kQ8Tokens) return Q8Kind::kToken;
+  if (T > kQ8LargeT) return Q8Kind::kSmall;
+  const Q8Tile b = q8_tile(T, true), m = q8_tile(T, false);
+  if (ceil_div(N, 32 * b.mb) * ceil_div(Dp, 128 * b.nb) >= 192) return Q8Kind::kBig;
+  const int64_t medium = ceil_div(N, 32 * m.mb) * ceil_div(Dp, 128 * m.nb);
+  return medium < 48 && q8_blocks(Cp) >= 4 ? Q8Kind::kSmall : Q8Kind::kMedium;
+}
+
 // Both entry points that write rows.
 int write_rows(bool norm, const void* x, const void* res, const void* gamma, void* sum, void* rows8, int64_t N, int64_t Cp,
                int T, float eps, int dtype, void* stream) {
@@ -125,15 +139,19 @@ int eqlinear_q8_fwd(const void* rows8, const void* w8, const void* bias, const v
   a.pitch = (int)q8_pitch(Cp);
   a.kblocks = (int)q8_blocks(Cp);
   a.Dpad = (int)q8_out(Dp);
-  const int64_t bm = 32 * q8_mb(T), bn = 128 * q8_nb(T);
-  const bool large = ceil_div(N, bm) * ceil_div(Dp, bn) >= 128;
-  const int64_t rowTiles = ceil_div(N, large ? bm : 32), colTiles = ceil_div(Dp, large ? bn : 32);
-  if (rowTiles * colTiles > kMaxGrid / 2) return EQL_EINVAL;
-  a.rowTiles = (int)rowTiles;
+  const Q8Kind kind = product_kind(N, Cp, Dp, T);
+  const Q8Tile tile = q8_tile(T, kind == Q8Kind::kBig);
+  const bool small = kind == Q8Kind::kSmall, token = kind == Q8Kind::kToken;
+  const int64_t rowTiles = token ? 1 : ceil_div(N, small ? 32 : 32 * tile.mb);
+  const int64_t colTiles = ceil_div(Dp, token ? 8 : (small ? 32 : 128 * tile.nb));
+  const int64_t grid = rowTiles * colTiles;
+  if (grid > kMaxGrid / 2) return EQL_EINVAL;
   a.colTiles = (int)colTiles;
-  const unsigned grid = (unsigned)(rowTiles * colTiles);
+  // Eight waves a tile while there is a compute unit for each (32 rows of 1024 -> 1024 channels: 5.9 us, with four 6.2),
+  // else four (300 rows: 15.8 and 13.7).
+  a.waves = (int)std::min<int64_t>(grid <= 256 ? q8_waves(T) : 4, ceil_div(a.pitch, 32));
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return status_of(dtype == EQL_F16 ? launch_q8_fwd_f16(T, large, a, grid, s) : launch_q8_fwd_f32(T, large, a, grid, s));
+  return status_of(dtype == EQL_F16 ? launch_q8_fwd_f16(T, kind, a, (unsigned)grid, s) : launch_q8_fwd_f32(T, kind, a, (unsigned)grid, s));
 }
 
 }  // extern "C"

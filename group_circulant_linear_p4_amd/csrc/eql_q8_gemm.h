@@ -1,7 +1,6 @@
 // The EQ-Linear layer on 8-bit integer rows and weights (eql_q8.h): for each plane of the half
 // spectrum integer products with 32-bit sums, which are exact (|sum| <= 2 C 127^2 < 2^31), then
-//     plane = sum * scale of the output channel * scale of the row
-// (in this order: rows near fp32's end stay finite),
+//     plane = sum * (scale of the output channel * scale of the row),
 // the inverse transform, and the fused layer's epilogue (bias, GELU, residual).  A row's outputs
 // depend on nothing but the row and the weight: sums are exact in any order, so every kernel and
 // every split gives the same bits.
@@ -27,7 +26,8 @@ struct Q8FwdArgs {
   const unsigned char* w;       // weight
   const float* wScales;         // [F][Dpad]
   int pitch, kblocks, Dpad;
-  int rowTiles, colTiles;
+  int colTiles;
+  int waves;                    // small kernel
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -41,31 +41,156 @@ __device__ __forceinline__ u32x4 q8_neg(const u32x4& v) {
   return ((n & 0x7F7F7F7Fu) + 0x01010101u) ^ (n & 0x80808080u);
 }
 
-// One K step of all planes: A and B operands of the T planes into the accumulators.
+#endif
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// The T outputs of one (row, output channel) before the activation: scaled planes, inverse transform,
+// bias.  sum * (scale of the channel * scale of the row) in one fused operation each where the transform's
+// coefficients are 0 and +-1, which also makes a cyclic shift exact (each output is the same expression).
 template <int T>
-__device__ __forceinline__ void q8_step(i32x16 (&acc)[T], const u32x4 (&a)[T], const u32x4 (&b)[T], const u32x4 (&neg)[n_pairs(T) + 1]) {
-  constexpr int NR = n_real_planes(T);
+__device__ __forceinline__ void q8_outputs(const int32_t (&sum)[T], const float (&scale)[n_freqs(T)], float bias, float (&y)[T],
+                                           const Twiddles& tw) {
+  if constexpr (T == 1) {
+    y[0] = __builtin_fmaf((float)sum[0], scale[0], bias);
+  } else if constexpr (T == 2 || T == 4) {
+    const float e = __builtin_fmaf((float)sum[0], scale[0], bias), a1 = (float)sum[1];
+    const float ep = __builtin_fmaf(a1, scale[1], e), em = __builtin_fmaf(-a1, scale[1], e);
+    if constexpr (T == 2) {
+      y[0] = ep;
+      y[1] = em;
+    } else {
+      const float re = (float)sum[2], im = (float)sum[3];
+      y[0] = __builtin_fmaf(re, scale[2], ep);
+      y[1] = __builtin_fmaf(-im, scale[2], em);
+      y[2] = __builtin_fmaf(-re, scale[2], ep);
+      y[3] = __builtin_fmaf(im, scale[2], em);
+    }
+  } else {
+    float P[T];
 #pragma unroll
-  for (int p = 0; p < NR; ++p) q8_mfma(acc[p], a[p], b[p]);
+    for (int p = 0; p < T; ++p) P[p] = (float)sum[p] * scale[freq_of(T, p)];
+    Idft<T, false>::run(P, y, tw);
 #pragma unroll
-  for (int q = 0; q < n_pairs(T); ++q) {
-    const int re = NR + 2 * q, im = re + 1;
-    q8_mfma(acc[re], a[re], b[re]);
-    q8_mfma(acc[im], a[re], b[im]);
-    q8_mfma(acc[re], a[im], neg[q]);
-    q8_mfma(acc[im], a[im], b[re]);
+    for (int g = 0; g < T; ++g) y[g] += bias;
   }
 }
 #endif
 
-// Few rows or few output channels: a workgroup takes a 32 x 32 tile of outputs, its waves every
-// W-th K block each (operands straight from memory, a block ahead), and adds its integer sums in
-// LDS.  Epilogue: a thread a (row, channel).
-template <int T, typename Elt, int W>
-__global__ void __launch_bounds__(64 * W) eql_q8_small_kernel(const Q8FwdArgs a) {
+// The fused layer's end for one (row, output channel).
+template <int T, typename Elt>
+__device__ __forceinline__ void q8_finish(const Q8FwdArgs& a, const int32_t (&sum)[T], const float (&scale)[n_freqs(T)], float bias,
+                                          const float (&res)[T], int64_t at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  float y[T];
+  q8_outputs<T>(sum, scale, bias, y, a.f.tw);
+#pragma unroll
+  for (int g = 0; g < T; ++g) y[g] = (a.f.act == 1 ? gelu_erf(y[g]) : y[g]) + res[g];
+  store_group<T, Elt>(static_cast<Elt*>(a.f.y) + at, y);
+#endif
+}
+
+// One to kQ8Tokens rows: nothing but the weight's bytes matters.  A workgroup takes eight output channels (128
+// bytes of every 512 in the weight's operand order), so that the weight spreads over the chip (1024 channels: 128
+// workgroups); lane l takes channel l % 8 and the 16 input channels number l / 8 of each pair of K blocks, its wave
+// every fourth pair.  Dot products of four codes, eight lanes' and four waves' sums added at the end.
+constexpr int kQ8Tokens = 4;
+template <int T, typename Elt>
+__global__ void __launch_bounds__(256) eql_q8_token_kernel(const Q8FwdArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NR = n_real_planes(T), NP = n_pairs(T), F = n_freqs(T);
+  __shared__ int32_t sums[kQ8Tokens][T][4][8];
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int ol = lane & 7, piece = lane >> 3;  // piece: K block of the pair, its half, quarter
+  const int col0 = (int)blockIdx.x * 8;
+  // The last eight threads' epilogue operands are on their way before the sums.
+  const int n = (int)threadIdx.x >> 3, col = col0 + ((int)threadIdx.x & 7);
+  const bool ends = n < a.f.N && n < kQ8Tokens && col < a.f.Dout;
+  float scale[F], res[T], bias = 0.0f;
+  const int64_t at = ((int64_t)n * a.f.Dout + col) * T;
+#pragma unroll
+  for (int g = 0; g < T; ++g) res[g] = 0.0f;
+  if (ends) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) scale[f] = a.wScales[(int64_t)f * a.Dpad + col] * a.rowScales[(int64_t)n * F + f];
+    if (a.f.bias) bias = (float)static_cast<const Elt*>(a.f.bias)[col];
+    if (a.f.res) load_group<T, Elt>(static_cast<const Elt*>(a.f.res) + at, res);
+  }
+  int32_t acc[kQ8Tokens][T + NP];
+#pragma unroll
+  for (int r = 0; r < kQ8Tokens; ++r)
+#pragma unroll
+    for (int p = 0; p < T + NP; ++p) acc[r][p] = 0;
+  const unsigned char* w = a.w + (size_t)(col0 / 32) * a.kblocks * T * 2048 + (size_t)((col0 & 31) + ol) * 16;
+  const int64_t rowBytes = (int64_t)a.pitch * T;
+  auto dot = [](int32_t& s, const u32x4& x, const u32x4& y) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_sdot4((int)x[i], (int)y[i], s, false);
+  };
+#pragma unroll 2
+  for (int kb = wave * 2 + (piece >> 2); kb < a.kblocks; kb += 8) {
+    const int k = kb * kQ8Block + (piece & 3) * 16;  // this lane's first input channel
+    if (k >= a.pitch) continue;                       // whole pieces: a row's planes are multiples of 16
+    u32x4 wv[T];
+#pragma unroll
+    for (int p = 0; p < T; ++p)
+      wv[p] = *reinterpret_cast<const u32x4*>(w + ((size_t)kb * T + p) * 2048 + (piece & 3) * 512);
+#pragma unroll
+    for (int r = 0; r < kQ8Tokens; ++r) {
+      if (r >= a.f.N) break;
+      u32x4 xv[T];
+#pragma unroll
+      for (int p = 0; p < T; ++p) xv[p] = *reinterpret_cast<const u32x4*>(a.codes + r * rowBytes + p * a.pitch + k);
+#pragma unroll
+      for (int p = 0; p < NR; ++p) dot(acc[r][p], xv[p], wv[p]);
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        const int re = NR + 2 * q, im = re + 1;
+        dot(acc[r][re], xv[re], wv[re]);
+        dot(acc[r][T + q], xv[im], wv[im]);  // subtracted at the end
+        dot(acc[r][im], xv[re], wv[im]);
+        dot(acc[r][im], xv[im], wv[re]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kQ8Tokens; ++r) {
+    if (r >= a.f.N) break;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) acc[r][NR + 2 * q] -= acc[r][T + q];
+#pragma unroll
+    for (int p = 0; p < T; ++p) {
+      // Lanes 8, 16 and 32 apart: within a row of 16 by a rotation, then the swaps of half rows and halves.
+      int32_t v = acc[r][p] + (int32_t)dpp_move<0x128>((uint32_t)acc[r][p]);
+      const auto h = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+      v = (int32_t)h[0] + (int32_t)h[1];
+      const auto g = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+      v = (int32_t)g[0] + (int32_t)g[1];
+      if (lane < 8) sums[r][p][wave][lane] = v;
+    }
+  }
+  __syncthreads();
+  if (!ends) return;
+  int32_t sum[T];
+#pragma unroll
+  for (int p = 0; p < T; ++p) {
+    sum[p] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[p] += sums[n][p][i][threadIdx.x & 7];
+  }
+  q8_finish<T, Elt>(a, sum, scale, bias, res, at);
+#endif
+}
+
+// Few rows or few output channels: a workgroup takes a 32 x 32 tile of outputs, its waves every so-manieth step
+// of 32 input channels each (operands straight from memory), and adds its integer sums in LDS.  Epilogue: a thread a
+// (row, channel), a row's channels on neighbouring lanes; its operands are on their way before the sums.
+template <int T, typename Elt>
+__global__ void __launch_bounds__(T <= 8 ? 512 : 256) eql_q8_small_kernel(const Q8FwdArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NR = n_real_planes(T), NP = n_pairs(T), F = n_freqs(T);
   __shared__ int32_t sums[T][32 * 32];
+  __shared__ float rowScale[32 * F];
+  const int threads = (int)blockDim.x, W = threads >> 6;
   const int colTile = (int)blockIdx.x % a.colTiles, rowTile = (int)blockIdx.x / a.colTiles;
   const int row0 = rowTile * 32;
   const int lane = lane_index(), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -74,81 +199,116 @@ __global__ void __launch_bounds__(64 * W) eql_q8_small_kernel(const Q8FwdArgs a)
   const uint32_t blockBytes = (uint32_t)T * 2048u;
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.codes + (size_t)row0 * rowBytes, (uint32_t)rows * rowBytes);
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (size_t)colTile * a.kblocks * blockBytes, (uint32_t)a.kblocks * blockBytes);
-  for (int i = (int)threadIdx.x; i < T * 1024; i += 64 * W) (&sums[0][0])[i] = 0;
   i32x16 acc[T];
 #pragma unroll
   for (int p = 0; p < T; ++p) acc[p] = (i32x16){};
   // Offsets past the last row's end (also of the last plane's last block) read as zero; bytes past
   // another plane's end belong to the next one and meet zeros in the weight.
   const uint32_t xOff = (uint32_t)(lane & 31) * rowBytes + (uint32_t)(lane >> 5) * 16u;
-  for (int kb = wave; kb < a.kblocks; kb += W) {
+  const int steps = (a.pitch + 31) / 32;
+  u32x4 xa[T], wb[T];
+  auto load = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 xa[T], wb[T], neg[NP + 1];
+    for (int p = 0; p < T; ++p) {
+      xa[p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, xOff + (uint32_t)(st * 32 + p * a.pitch), 0, 0));
+      wb[p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16 + p * 2048, (st >> 1) * (int)blockBytes + (st & 1) * 1024, 0));
+    }
+  };
+  if (wave < steps) load(wave);
+  // What the epilogue reads, and zeros, while the first operands come.
+  const int col = colTile * 32 + ((int)threadIdx.x & 31), at = min(col, a.f.Dout - 1);
+  float ws[F];
 #pragma unroll
-      for (int p = 0; p < T; ++p) {
-        xa[p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, xOff + (uint32_t)(kb * 64 + s * 32 + p * a.pitch), 0, 0));
-        wb[p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16 + (p * 2 + s) * 1024, kb * (int)blockBytes, 0));
-      }
+  for (int f = 0; f < F; ++f) ws[f] = a.wScales[(int64_t)f * a.Dpad + at];
+  const float bias = a.f.bias ? (float)static_cast<const Elt*>(a.f.bias)[at] : 0.0f;
+  for (int i = (int)threadIdx.x; i < rows * F; i += threads) rowScale[i] = a.rowScales[(int64_t)row0 * F + i];
+  for (int i = (int)threadIdx.x; i < T * 256; i += threads) reinterpret_cast<i32x4*>(&sums[0][0])[i] = (i32x4){0, 0, 0, 0};
+  for (int st = wave; st < steps; st += W) {
+    u32x4 x[T], w[T];
 #pragma unroll
-      for (int q = 0; q < NP; ++q) neg[q] = q8_neg(wb[NR + 2 * q + 1]);
-      q8_step<T>(acc, xa, wb, neg);
+    for (int p = 0; p < T; ++p) {
+      x[p] = xa[p];
+      w[p] = wb[p];
+    }
+    if (st + W < steps) load(st + W);
+#pragma unroll
+    for (int p = 0; p < NR; ++p) q8_mfma(acc[p], x[p], w[p]);
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      const int re = NR + 2 * q, im = re + 1;
+      const u32x4 neg = q8_neg(w[im]);
+      q8_mfma(acc[re], x[re], w[re]);
+      q8_mfma(acc[im], x[re], w[im]);
+      q8_mfma(acc[re], x[im], neg);
+      q8_mfma(acc[im], x[im], w[re]);
     }
   }
   __syncthreads();
-#pragma unroll
-  for (int p = 0; p < T; ++p)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (row < rows) __hip_atomic_fetch_add(&sums[p][row * 32 + (lane & 31)], acc[p][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-    }
-  __syncthreads();
-  for (int i = (int)threadIdx.x; i < rows * 32; i += 64 * W) {
-    const int row = row0 + (i >> 5), col = colTile * 32 + (i & 31);
-    if (col >= a.f.Dout) continue;
-    float P[T], y[T];
+  if (wave < steps) {
 #pragma unroll
     for (int p = 0; p < T; ++p)
-      P[p] = (float)sums[p][i] * a.wScales[(int64_t)freq_of(T, p) * a.Dpad + col] * a.rowScales[(int64_t)row * F + freq_of(T, p)];
-    Idft<T, false>::run(P, y, a.f.tw);
-    const float bias = a.f.bias ? (float)static_cast<const Elt*>(a.f.bias)[col] : 0.0f;
-    const int64_t at = ((int64_t)row * a.f.Dout + col) * T;
-    float r[T];
 #pragma unroll
-    for (int g = 0; g < T; ++g) r[g] = 0.0f;
-    if (a.f.res) load_group<T, Elt>(static_cast<const Elt*>(a.f.res) + at, r);
+      for (int r = 0; r < 16; ++r) {
+        const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (row < rows) __hip_atomic_fetch_add(&sums[p][row * 32 + (lane & 31)], acc[p][r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      }
+  }
+  __syncthreads();
+  if (col >= a.f.Dout) return;
+  for (int row = (int)threadIdx.x >> 5; row < rows; row += threads >> 5) {
+    const int64_t out = ((int64_t)(row0 + row) * a.f.Dout + col) * T;
+    float scale[F], res[T];
+    int32_t sum[T];
 #pragma unroll
-    for (int g = 0; g < T; ++g) {
-      const float v = y[g] + bias;
-      y[g] = (a.f.act == 1 ? gelu_erf(v) : v) + r[g];
-    }
-    store_group<T, Elt>(static_cast<Elt*>(a.f.y) + at, y);
+    for (int g = 0; g < T; ++g) res[g] = 0.0f;
+    if (a.f.res) load_group<T, Elt>(static_cast<const Elt*>(a.f.res) + out, res);
+#pragma unroll
+    for (int p = 0; p < T; ++p) sum[p] = sums[p][row * 32 + (col & 31)];
+#pragma unroll
+    for (int f = 0; f < F; ++f) scale[f] = ws[f] * rowScale[row * F + f];
+    q8_finish<T, Elt>(a, sum, scale, bias, res, out);
   }
 #endif
 }
 
-// Rows of a workgroup of the large kernel: WM waves down, MB blocks of 32 each.  Waves across: 4 / WM,
-// NB blocks of 32 output channels each.
-//   * Rows' codes go through LDS, two slots of one K block (64 input channels of every plane): loads
-//     that write LDS directly, 1 KB (16 rows x 64 bytes of a plane) each.  Piece q (16 bytes) of row r
-//     lies at place q ^ (r / 4) % 4 of its 64 bytes, so the 16 rows that a fragment read takes at a
-//     time touch every bank once.
-//   * The weight's operands are read by no other wave of the row block, and lie in memory as the
-//     matrix instruction wants them: each wave loads its own straight into registers.
-//   * While a K block is multiplied, the next one's rows and operands are on their way.
+// Many rows: a workgroup takes a tile of 32 MB WM rows x 32 NB (4 / WM) output channels of all planes, its
+// four waves WM down and 4 / WM across, MB x NB blocks of 32 x 32 each.
+//   * Rows' codes go through an LDS ring of four slots, a K block (64 input channels of every plane) each, by
+//     loads that write LDS directly (1 KB: 16 rows x 64 bytes of a plane), three blocks ahead.  Piece q (16
+//     bytes) of row r lies at place q ^ (r / 4) % 4 of its 64 bytes, so the 16 rows that a fragment read takes
+//     at a time touch every bank once.  The slots are separate arrays and every slot's code is its own, so
+//     the compiler knows which loads a read of LDS has to wait for.
+//   * The weight's operands lie in memory as the matrix instruction wants them, and no two waves across read
+//     the same: each wave loads its own straight into registers, a block ahead (more than six planes' blocks:
+//     each plane's next step as soon as this one's products have been issued).
+//   * A block is 2 MB groups (a step of 32 input channels, 32 rows) of products.  Each plane of the next
+//     group's rows is read from LDS as soon as this group's products of the plane have been issued; at the last
+//     group from the next slot, so the wait for its loads and the barrier come before that group's products.
 template <int T, typename Elt, int MB, int NB, int WM>
-__global__ void __launch_bounds__(256) eql_q8_large_kernel(const Q8FwdArgs a) {
+__global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_kernel(const Q8FwdArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NR = n_real_planes(T), NP = n_pairs(T), F = n_freqs(T);
-  constexpr int BM = 32 * MB * WM, WN = 4 / WM;
+  constexpr int BM = 32 * MB * WM, WN = 4 / WM, NS = 4;
   constexpr int CHUNKS = T * BM / 16;              // 1 KB loads of a slot
-  constexpr int PER = (CHUNKS + 3) / 4;            // of a wave
-  constexpr int SLOT = CHUNKS * 1024;
-  static_assert(BM <= kFwdRows, "the epilogue's rows");
-  static_assert(2 * SLOT + F * BM * 4 <= 160 * 1024, "LDS");
-  __shared__ u32x4 ring[2][SLOT / 16];
-  __shared__ float rowScale[F][BM];
+  constexpr int PER = (CHUNKS + 3) / 4;            // of a wave (where four do not divide them, some twice)
+  constexpr int SLOT = CHUNKS * 64;                // 16-byte pieces
+  constexpr int SCALES = (BM * F * 4 + 1023) / 1024;  // 1 KB loads of the rows' scales
+  constexpr bool WHOLE = T * NB <= 6;
+  constexpr int WSETS = WHOLE ? 2 : 1, WSTEPS = WHOLE ? 2 : 1;
+  constexpr int WLOADS = WSTEPS * NB * T;          // operand loads of a set
+  static_assert(BM <= kFwdRows && (NS * SLOT + SCALES * 64) * 16 <= 160 * 1024, "LDS");
+  typedef __attribute__((address_space(3))) void* Lds;
+
+  __shared__ u32x4 ring0[SLOT], ring1[SLOT], ring2[SLOT], ring3[SLOT];
+  __shared__ u32x4 scaleRing[SCALES * 64];
+  const float* rowScale = reinterpret_cast<const float*>(scaleRing);
+  auto slot_of = [&](auto tag) __attribute__((always_inline)) -> u32x4* {
+    constexpr int S = decltype(tag)::value % NS;
+    if constexpr (S == 0) return ring0;
+    else if constexpr (S == 1) return ring1;
+    else if constexpr (S == 2) return ring2;
+    else return ring3;
+  };
 
   const int tile = xcd_remap((int)blockIdx.x, (int)gridDim.x);
   const int colTile = tile % a.colTiles, rowTile = tile / a.colTiles;
@@ -156,51 +316,54 @@ __global__ void __launch_bounds__(256) eql_q8_large_kernel(const Q8FwdArgs a) {
   const int rows = min(BM, a.f.N - row0);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
-  const int lane = lane_index();
+  const int lane = (int)threadIdx.x & 63, lrow = lane & 31;
   const int block0 = (colTile * WN + wn) * NB;     // this wave's first block of 32 output channels
   const int nblk = a.Dpad / 32;
   const uint32_t rowBytes = (uint32_t)a.pitch * T;
   const uint32_t blockBytes = (uint32_t)T * 2048u;
   const uint32_t colBytes = (uint32_t)a.kblocks * blockBytes;
 
-  for (int i = (int)threadIdx.x; i < F * BM; i += 256) {
-    const int f = i / BM, r = i - f * BM;
-    rowScale[f][r] = r < rows ? a.rowScales[((int64_t)row0 + r) * F + f] : 0.0f;
+  {
+    // Rows past N have the scale zero.
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.rowScales + (int64_t)row0 * F, (uint32_t)rows * F * 4u);
+#pragma unroll
+    for (int i = 0; i < (SCALES + 3) / 4; ++i) {
+      const int j = min(wave + 4 * i, SCALES - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds)(scaleRing + j * 64), 16, j * 1024 + lane * 16, 0, 0, 0);
+    }
   }
-
-  // Rows past N and (at the last row's end) bytes past the codes read as zero; bytes past a plane's
-  // end belong to the next one and meet zeros in the weight.
-  const uint64_t xBase = reinterpret_cast<uint64_t>(a.codes) + (uint64_t)row0 * rowBytes;
+  // Rows past N and, at the last row's end, bytes past the codes read as zero; bytes past a plane's end belong
+  // to the next one and meet zeros in the weight.  Blocks past the last one are outside of the range.
+  const char* xBase = reinterpret_cast<const char*>(a.codes) + (size_t)row0 * rowBytes;
   const uint32_t xBytes = (uint32_t)rows * rowBytes;
   uint32_t xOff[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int j = wave * PER + i, p = j / (BM / 16), rg = j % (BM / 16);
+    const int j = min(wave * PER + i, CHUNKS - 1), p = j / (BM / 16), rg = j % (BM / 16);
     const int r = rg * 16 + (lane >> 2), q = (lane & 3) ^ ((r >> 2) & 3);
-    xOff[i] = j < CHUNKS ? (uint32_t)r * rowBytes + (uint32_t)p * (uint32_t)a.pitch + (uint32_t)q * 16u : kOob;
+    xOff[i] = (uint32_t)r * rowBytes + (uint32_t)p * (uint32_t)a.pitch + (uint32_t)q * 16u;
   }
-  const uint32_t ringAt = lds_addr(&ring[0][0]) + (uint32_t)wave * PER * 1024u;
-  auto issue_rows = [&](int kb, int slot) __attribute__((always_inline)) {
+  auto issue_rows = [&](int kb, u32x4* slot, int i0, int i1) __attribute__((always_inline)) {
     const uint32_t skip = (uint32_t)kb * 64u;
-    const BufDesc d = desc_at(xBase + skip, xBytes - skip);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(xBase + skip, kb < a.kblocks ? xBytes - skip : 0u);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (CHUNKS % 4 == 0 || wave * PER + i < CHUNKS) dma16(d, xOff[i], ringAt + (uint32_t)slot * SLOT + (uint32_t)i * 1024u);
+    for (int i = i0; i < i1; ++i) {
+      const int j = min(wave * PER + i, CHUNKS - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds)(slot + j * 64), 16, (int)xOff[i], 0, 0, 0);
+    }
   };
 
-  // Blocks past the last one read the last one's operands, and store nothing.
+  // Blocks of output channels past the last one read the last one's operands, and store nothing.
   const int first = min(block0, nblk - 1), more = nblk - 1 - first;
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w + (size_t)first * colBytes, (uint32_t)(min(NB - 1, more) + 1) * colBytes);
-  u32x4 wb[2][2][NB][T];
-  auto load_w = [&](int kb, u32x4 (&to)[2][NB][T]) __attribute__((always_inline)) {
+  u32x4 wb[WSETS][WSTEPS][NB][T];
+  auto load_w1 = [&](int kb, int s, int nb, int p) __attribute__((always_inline)) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+        wr, lane * 16, min(kb, a.kblocks - 1) * (int)blockBytes + min(nb, more) * (int)colBytes + (p * 2 + s) * 1024, 0));
+  };
+  auto load_w = [&](int kb, u32x4 (&to)[WSTEPS][NB][T], int i0, int i1) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int p = 0; p < T; ++p)
-          to[s][nb][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-              wr, lane * 16 + (p * 2 + s) * 1024, kb * (int)blockBytes + min(nb, more) * (int)colBytes, 0));
+    for (int i = i0; i < i1; ++i) to[i / (NB * T)][i / T % NB][i % T] = load_w1(kb, i / (NB * T), i / T % NB, i % T);
   };
 
   i32x16 acc[MB][NB][T];
@@ -211,72 +374,167 @@ __global__ void __launch_bounds__(256) eql_q8_large_kernel(const Q8FwdArgs a) {
 #pragma unroll
       for (int p = 0; p < T; ++p) acc[mb][nb][p] = (i32x16){};
 
-  const int lrow = lane & 31;
-  auto read_rows = [&](int slot, int s, int mb, u32x4 (&xa)[T]) __attribute__((always_inline)) {
+  u32x4 xa[T];
+  auto read_row = [&](const u32x4* slot, int s, int mb, int p) __attribute__((always_inline)) {
     const int r = (wm * MB + mb) * 32 + lrow;
     const int q = (s * 2 + (lane >> 5)) ^ ((r >> 2) & 3);
-#pragma unroll
-    for (int p = 0; p < T; ++p) xa[p] = ring[slot][p * (BM * 4) + r * 4 + q];
+    xa[p] = slot[p * (BM * 4) + r * 4 + q];
   };
 
-  auto stage = [&](int kb, auto curTag) __attribute__((always_inline)) {
-    constexpr int cur = decltype(curTag)::value;
-    if (kb + 1 < a.kblocks) {
-      issue_rows(kb + 1, cur ^ 1);
-      load_w(kb + 1, wb[cur ^ 1]);
-    }
+  constexpr int GROUPS = 2 * MB, ISSUE = GROUPS > 2 ? GROUPS / 2 : 1;  // groups that issue the loads ahead
+  // Loads of this wave that may be under way when the next block's rows have to be there: at least so many have
+  // been issued after them (two blocks' rows, and the operands of two blocks, or of two steps; before the first
+  // block the order is rows 0, rows 1, operands, rows 2).
+  constexpr int AHEAD = 2 * PER + 2 * WLOADS;
+  auto stage = [&](int kb, auto tag) __attribute__((always_inline)) {
+    constexpr int S = decltype(tag)::value, wcur = WHOLE ? S & 1 : 0;
+    const u32x4* cur = slot_of(tag);
+    const u32x4* nxt = slot_of(std::integral_constant<int, S + 1>{});
+    u32x4* ahead = slot_of(std::integral_constant<int, S + NS - 1>{});
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 neg[NB][NP + 1];
+    for (int g = 0; g < GROUPS; ++g) {
+      const int s = g / MB, mb = g % MB, ws = WHOLE ? s : 0;
+      if (g < ISSUE) {
+        issue_rows(kb + NS - 1, ahead, g * PER / ISSUE, (g + 1) * PER / ISSUE);
+        if constexpr (WHOLE) load_w(kb + 1, wb[wcur ^ 1], g * WLOADS / ISSUE, (g + 1) * WLOADS / ISSUE);
+      }
+      if (g + 1 == GROUPS) {
+        // The next block's rows are in LDS, and every wave has read this one's.
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<(AHEAD < 63 ? AHEAD : 63)>();
+        wait_lgkm0();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
+      // What the last block reads ahead is not used.
+      auto next = [&](int p) __attribute__((always_inline)) {
+        if (g + 1 < GROUPS) read_row(cur, (g + 1) / MB, (g + 1) % MB, p);
+        else read_row(nxt, 0, 0, p);
+        if constexpr (!WHOLE) {
+          if (mb + 1 == MB) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb) wb[0][0][nb][p] = load_w1(kb + s, s ^ 1, nb, p);
+          }
+        }
+      };
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < NP; ++q) neg[nb][q] = q8_neg(wb[cur][s][nb][NR + 2 * q + 1]);
+      for (int p = 0; p < NR; ++p) {
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        u32x4 xa[T];
-        read_rows(cur, s, mb, xa);
+        for (int nb = 0; nb < NB; ++nb) q8_mfma(acc[mb][nb][p], xa[p], wb[wcur][ws][nb][p]);
+        next(p);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) q8_step<T>(acc[mb][nb], xa, wb[cur][s][nb], neg[nb]);
+      for (int q = 0; q < NP; ++q) {
+        const int re = NR + 2 * q, im = re + 1;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const u32x4(&w)[T] = wb[wcur][ws][nb];
+          const u32x4 neg = q8_neg(w[im]);
+          q8_mfma(acc[mb][nb][re], xa[re], w[re]);
+          q8_mfma(acc[mb][nb][im], xa[re], w[im]);
+          q8_mfma(acc[mb][nb][re], xa[im], neg);
+          q8_mfma(acc[mb][nb][im], xa[im], w[re]);
+        }
+        next(re);
+        next(im);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    // The next block's rows are in LDS, and every wave is done with this one's.
-    wait_vmcnt<0>();
-    wait_lgkm0();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
   };
 
-  issue_rows(0, 0);
-  load_w(0, wb[0]);
-  wait_vmcnt<0>();
-  __syncthreads();
-  int kb = 0;
-  for (; kb + 2 <= a.kblocks; kb += 2) {
-    stage(kb, std::integral_constant<int, 0>{});
-    stage(kb + 1, std::integral_constant<int, 1>{});
+  // Epilogue in chunks of CH rows: outputs past the rows or channels get an offset beyond the descriptor's
+  // range.  A chunk's residual is loaded while the one before is finished (and before the chunk's own stores:
+  // it may be y); without one its range is empty.
+  constexpr int ELT = (int)sizeof(Elt);
+  constexpr int RW = group_words<T, Elt>(), CH = T > 8 ? 1 : (RW <= 2 ? 16 : (RW <= 4 ? 8 : 4)), PARTS = 16 / CH;
+  const uint32_t outRow = (uint32_t)a.f.Dout * T * ELT;
+  const __amdgpu_buffer_rsrc_t yr = make_rsrc(static_cast<char*>(a.f.y) + (size_t)row0 * outRow, (uint32_t)rows * outRow);
+  const __amdgpu_buffer_rsrc_t rr =
+      make_rsrc(static_cast<const char*>(a.f.res) + (size_t)row0 * outRow, a.f.res ? (uint32_t)rows * outRow : 0u);
+  constexpr bool EARLY = T * MB * NB <= 4 && CH * RW <= 32;
+  uint32_t res[2][CH][RW];
+  auto offset_of = [&](int nb, int mb, int r) __attribute__((always_inline)) {
+    const int col = (block0 + nb) * 32 + lrow, row = (wm * MB + mb) * 32 + 4 * (lane >> 5);
+    const uint32_t off = col < a.f.Dout ? (uint32_t)row * outRow + (uint32_t)(col * T * ELT) : kOob;
+    return off + (uint32_t)(8 * (r >> 2) + (r & 3)) * outRow;
+  };
+  auto load_res = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      load_group_raw<T, Elt>(rr, offset_of(i / PARTS / MB, i / PARTS % MB, i % PARTS * CH + j), res[i & 1][j]);
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
+  // What the epilogue reads of the output channels, and where registers are left its first residuals.
+  float ws[NB][F], bias[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int col = (block0 + nb) * 32 + lrow;
+#pragma unroll
+    for (int f = 0; f < F; ++f) ws[nb][f] = a.wScales[(int64_t)f * a.Dpad + min(col, a.Dpad - 1)];
+    bias[nb] = a.f.bias ? (float)static_cast<const Elt*>(a.f.bias)[min(col, a.f.Dout - 1)] : 0.0f;
   }
-  if (kb < a.kblocks) stage(kb, std::integral_constant<int, 0>{});
+  if constexpr (EARLY) load_res(0);
+  __builtin_amdgcn_sched_barrier(0);
+  issue_rows(0, ring0, 0, PER);
+  __builtin_amdgcn_sched_barrier(0);
+  issue_rows(1, ring1, 0, PER);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(0, wb[0], 0, WLOADS);
+  issue_rows(2, ring2, 0, PER);
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vmcnt<(2 * PER + WLOADS < 63 ? 2 * PER + WLOADS : 63)>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int p = 0; p < T; ++p) read_row(ring0, 0, 0, p);
+  for (int kb = 0;;) {
+    stage(kb, I0{});
+    if (++kb >= a.kblocks) break;
+    stage(kb, I1{});
+    if (++kb >= a.kblocks) break;
+    stage(kb, I2{});
+    if (++kb >= a.kblocks) break;
+    stage(kb, I3{});
+    if (++kb >= a.kblocks) break;
+  }
 
-  // Scales, and the fused layer's epilogue for each block of 32 rows.
+  auto finish = [&](auto geluTag) __attribute__((always_inline)) {
+    constexpr bool GELU = decltype(geluTag)::value;
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    f32x16 out[T][NB];
-    const int rowOff = (wm * MB + mb) * 32;
+    for (int i = 0; i < NB * MB * PARTS; ++i) {
+      const int nb = i / PARTS / MB, mb = i / PARTS % MB, c = i % PARTS * CH;
+      if (i + 1 < NB * MB * PARTS) load_res(i + 1);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int col = min((block0 + nb) * 32 + lrow, a.Dpad - 1);
+      for (int j = 0; j < CH; ++j) {
+        const int r = c + j, row = (wm * MB + mb) * 32 + 4 * (lane >> 5) + 8 * (r >> 2) + (r & 3);
+        int32_t sum[T];
+        float scale[F], y[T], v[T];
 #pragma unroll
-      for (int p = 0; p < T; ++p) {
-        const float ws = a.wScales[(int64_t)freq_of(T, p) * a.Dpad + col];
+        for (int p = 0; p < T; ++p) sum[p] = acc[mb][nb][p][r];
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          out[p][nb][r] = (float)acc[mb][nb][p][r] * ws * rowScale[freq_of(T, p)][rowOff + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)];
+        for (int f = 0; f < F; ++f) scale[f] = ws[nb][f] * rowScale[row * F + f];
+        q8_outputs<T>(sum, scale, bias[nb], y, a.f.tw);
+        group_from_raw<T, Elt>(res[i & 1][j], v);
+#pragma unroll
+        for (int g = 0; g < T; ++g) y[g] = (GELU ? gelu_erf(y[g]) : y[g]) + v[g];
+        store_group_buf<T, Elt>(yr, offset_of(nb, mb, r), y);
+        // A few rows at a time: all interleaved, their sums leave the accumulators together and spill.
+        if (T > 8 || (j & 3) == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }
-    fwd_epilogue<T, Elt, NB, 1>(a.f, out, row0, rowOff, block0 * 32);
-  }
+  };
+  // No load into LDS outlives the workgroup: the residuals' wait covers the older loads.
+  if constexpr (EARLY) wait_vmcnt<0>();
+  else load_res(0);
+  if (a.f.act == 1) finish(std::true_type{});
+  else finish(std::false_type{});
 #endif
 }
 

@@ -3,8 +3,8 @@
 
 namespace eql {
 
-hipError_t launch_q8_fwd_f32(int T, bool large, const Q8FwdArgs& a, unsigned grid, hipStream_t s) {
-  return q8_fwd_launch<float>(T, large, a, grid, s);
+hipError_t launch_q8_fwd_f32(int T, Q8Kind kind, const Q8FwdArgs& a, unsigned grid, hipStream_t s) {
+  return q8_fwd_launch<float>(T, kind, a, grid, s);
 }
 
 }  // namespace eql

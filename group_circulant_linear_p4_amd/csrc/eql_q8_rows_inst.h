@@ -14,11 +14,11 @@ static const void* q8_rows_fn(NormShape sh) {
     if (sh.k == 2) return sh.lpr == 64 ? (const void*)&eql_q8_rows_kernel<Elt, T, 64, 2> : (const void*)&eql_q8_rows_kernel<Elt, T, 256, 2>;
   }
   if constexpr (KEEP >= 4) {
-    if (sh.k == 4) return sh.lpr == 64 ? (const void*)&eql_q8_rows_kernel<Elt, T, 64, 4> : (const void*)&eql_q8_rows_kernel<Elt, T, 256, 4>;
+    if (sh.k == 4) return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 4>;
   }
   if (sh.k == 1) {
     if (sh.lpr == 64) return (const void*)&eql_q8_rows_kernel<Elt, T, 64, 1>;
-    if constexpr (KEEP <= 2) return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 1>;
+    return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 1>;
   }
   return nullptr;
 }
