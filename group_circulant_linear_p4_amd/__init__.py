@@ -162,20 +162,19 @@ _raw_stream = None
 
 def _current_stream():
     """The handle of torch's current stream.  A Stream object costs 3 us to make, most of a small
-    call; torch also hands out the bare handle, in a tenth of that."""
+    call; torch also hands out the bare handle, in a tenth of that, once its GPU side is up."""
     global _raw_stream
     import torch
-    if _raw_stream is None:
-        raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-        _raw_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
     if not torch.cuda.is_initialized():
         return torch.cuda.current_stream().cuda_stream
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    _raw_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
     return _raw_stream()
 
 
 def _stream(stream):
     if stream is None:
-        return _current_stream() or None
+        return (_raw_stream or _current_stream)() or None
     if isinstance(stream, int):
         return stream or None
     return getattr(stream, "cuda_stream", stream) or None

@@ -50,14 +50,25 @@ __device__ __forceinline__ float q8_top(uint32_t bits) {
 // 127 / m as the codes are defined: the reciprocal and the product each rounded.
 __device__ __forceinline__ float q8_inv(float m) { return 127.0f * (1.0f / m); }
 
-// Four codes of v * inv as a word.  The product is rounded to fp32, then adding 1.5 2^23 rounds it
+// Four codes as a word, of values times their 127 / m.  The product is rounded to fp32, then adding 1.5 2^23 rounds it
 // to an integer (ties to even), which is in the sum's low bits.  With inv a NaN the codes are not
 // specified (their scale is NaN).
-__device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float d, float inv) {
-  const uint32_t w0 = __builtin_bit_cast(uint32_t, a * inv + 12582912.0f), w1 = __builtin_bit_cast(uint32_t, b * inv + 12582912.0f);
-  const uint32_t w2 = __builtin_bit_cast(uint32_t, c * inv + 12582912.0f), w3 = __builtin_bit_cast(uint32_t, d * inv + 12582912.0f);
+__device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float d) {
+  const uint32_t w0 = __builtin_bit_cast(uint32_t, a + 12582912.0f), w1 = __builtin_bit_cast(uint32_t, b + 12582912.0f);
+  const uint32_t w2 = __builtin_bit_cast(uint32_t, c + 12582912.0f), w3 = __builtin_bit_cast(uint32_t, d + 12582912.0f);
   const uint32_t lo = __builtin_amdgcn_perm(w1, w0, 0x0c0c0400u), hi = __builtin_amdgcn_perm(w3, w2, 0x04000c0cu);
   return lo | hi;
+}
+
+// Transposes the 4 x 4 bytes of a quad of lanes: lane i gets byte i of each lane's word, lane 0's lowest.
+__device__ __forceinline__ uint32_t quad_transpose(uint32_t w) {
+  const int i = (int)threadIdx.x & 3;
+  // Lanes 1 apart: even lanes keep their bytes 0 and 2 and take the other's, odd ones 1 and 3.
+  const uint32_t o = dpp_move<kDppXor1>(w);
+  w = __builtin_amdgcn_perm(o, w, i & 1 ? 0x03070105u : 0x06020400u);
+  // Lanes 2 apart: lanes 0 and 1 keep the low halves, lanes 2 and 3 the high ones.
+  const uint32_t q = dpp_move<kDppXor2>(w);
+  return __builtin_amdgcn_perm(q, w, i & 2 ? 0x03020706u : 0x05040100u);
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
@@ -94,54 +105,60 @@ struct Q8RowsArgs {
   Twiddles tw;
 };
 
-// Channels that a lane takes at a time: 16 features or more, and whole words of codes.
-__host__ __device__ constexpr int q8_chunk(int T) { return T == 1 ? 16 : (T == 2 ? 8 : 4); }
-// Chunks that a lane holds at most (64 planes' values).
-__host__ __device__ constexpr int q8_keep(int T) { return T <= 4 ? 4 : (T <= 8 ? 2 : 1); }
+// Channels that a lane takes at a time.  Where 4 to 16 of them are at most 32 bytes, as many (whole words of codes);
+// else one, and a quad of lanes exchanges bytes to make words: with more bytes between neighbouring lanes a load
+// touches a line a lane (16384 rows of 64 channels, T = 8 fp32, the norm: 69 us with four channels a lane).
+__host__ __device__ constexpr int q8_chunk(int T, int elt) {
+  return elt == 2 ? (T == 1 ? 16 : (T == 2 ? 8 : (T <= 4 ? 4 : 1))) : (T == 1 ? 8 : (T == 2 ? 4 : 1));
+}
+// Chunks that a lane holds at most (64 values), and where a row is not spread over more lanes (32).
+__host__ __device__ constexpr int q8_keep(int T, int elt) {
+  const int n = 64 / (q8_chunk(T, elt) * T);
+  return n >= 8 ? 8 : 4;
+}
+__host__ __device__ constexpr int q8_some(int T, int elt) {
+  const int n = 32 / (q8_chunk(T, elt) * T);
+  return n >= 4 ? 4 : (n >= 2 ? 2 : 1);
+}
 
-// The E elements at p (at element alignment) to floats.
-template <typename Elt, int E>
+// The E elements at p (at element alignment) to floats, and back: pieces of 16 bytes, then 4, 2 and 1.
+template <typename Elt, int E, int FROM = 0>
 __device__ __forceinline__ void load_elts(const Elt* p, float (&v)[E]) {
-  static_assert(E % 4 == 0, "whole words");
-  if constexpr (E % 8 == 0) {
+  constexpr int N = E - FROM >= 8 && sizeof(Elt) == 2 ? 8 : (E - FROM >= 4 ? 4 : (E - FROM >= 2 ? 2 : 1));
+  if constexpr (E - FROM > 0) {
+    if constexpr (N == 1) {
+      v[FROM] = (float)p[FROM];
+    } else {
+      typedef Elt EN __attribute__((ext_vector_type(N), aligned(sizeof(Elt))));
+      const EN u = *reinterpret_cast<const EN*>(p + FROM);
 #pragma unroll
-    for (int i = 0; i < E; i += 8) {
-      const typename Chunk<Elt>::V u = *reinterpret_cast<const typename Chunk<Elt>::VU*>(p + i);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i + e] = (float)u[e];
+      for (int e = 0; e < N; ++e) v[FROM + e] = (float)u[e];
     }
-  } else {
-    typedef Elt E4 __attribute__((ext_vector_type(4), aligned(sizeof(Elt))));
-#pragma unroll
-    for (int i = 0; i < E; i += 4) {
-      const E4 u = *reinterpret_cast<const E4*>(p + i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[i + e] = (float)u[e];
-    }
+    load_elts<Elt, E, FROM + N>(p, v);
   }
 }
-template <typename Elt, int E>
+template <typename Elt, int E, int FROM = 0>
 __device__ __forceinline__ void store_elts(Elt* p, const float (&v)[E]) {
-  if constexpr (E % 8 == 0) {
+  constexpr int N = E - FROM >= 8 && sizeof(Elt) == 2 ? 8 : (E - FROM >= 4 ? 4 : (E - FROM >= 2 ? 2 : 1));
+  if constexpr (E - FROM > 0) {
+    if constexpr (N == 1) {
+      p[FROM] = (Elt)v[FROM];
+    } else {
+      typedef Elt EN __attribute__((ext_vector_type(N), aligned(sizeof(Elt))));
+      EN u;
 #pragma unroll
-    for (int i = 0; i < E; i += 8) {
-      typename Chunk<Elt>::VU u;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = (Elt)v[i + e];
-      __builtin_nontemporal_store(u, reinterpret_cast<typename Chunk<Elt>::VU*>(p + i));
+      for (int e = 0; e < N; ++e) u[e] = (Elt)v[FROM + e];
+      __builtin_nontemporal_store(u, reinterpret_cast<EN*>(p + FROM));
     }
-  } else {
-    typedef Elt E4 __attribute__((ext_vector_type(4), aligned(sizeof(Elt))));
-#pragma unroll
-    for (int i = 0; i < E; i += 4) __builtin_nontemporal_store((E4){(Elt)v[i], (Elt)v[i + 1], (Elt)v[i + 2], (Elt)v[i + 3]}, reinterpret_cast<E4*>(p + i));
+    store_elts<Elt, E, FROM + N>(p, v);
   }
 }
 
 // Chunk at channel c0 of a row: its values (zero past C) after the residual's addition, which it
 // stores.  `again`: the second reading of a row that is not held in registers.
 template <typename Elt, int T>
-__device__ __forceinline__ void q8_load(const Q8RowsArgs& a, int64_t row, int c0, bool again, float (&v)[q8_chunk(T) * T]) {
-  constexpr int CH = q8_chunk(T), E = CH * T;
+__device__ __forceinline__ void q8_load(const Q8RowsArgs& a, int64_t row, int c0, bool again, float (&v)[q8_chunk(T, sizeof(Elt)) * T]) {
+  constexpr int CH = q8_chunk(T, sizeof(Elt)), E = CH * T;
   const int64_t at = row * ((int64_t)a.C * T) + (int64_t)c0 * T;
   const bool kept = again && a.sum;
   const Elt* x = static_cast<const Elt*>(kept ? a.sum : a.x) + at;
@@ -162,12 +179,13 @@ __device__ __forceinline__ void q8_load(const Q8RowsArgs& a, int64_t row, int c0
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         const int e = c * T + t;
-        v[e] = 0.0f;
+        float q = 0.0f;
         if (c0 + c < a.C) {
-          v[e] = (float)x[e];
-          if (r) v[e] = (float)(Elt)(v[e] + (float)r[e]);
-          if (out) out[e] = (Elt)v[e];
+          q = (float)x[e];
+          if (r) q = (float)(Elt)(q + (float)r[e]);
+          if (out) out[e] = (Elt)q;
         }
+        v[e] = q;
       }
   }
 }
@@ -175,9 +193,9 @@ __device__ __forceinline__ void q8_load(const Q8RowsArgs& a, int64_t row, int c0
 // That chunk's planes, times the norm's weight; `top` collects each frequency's largest magnitude,
 // `sq` the sum of squares of the values.
 template <typename Elt, int T>
-__device__ __forceinline__ void q8_planes(const Q8RowsArgs& a, int c0, const float (&v)[q8_chunk(T) * T],
-                                          float (&pl)[T][q8_chunk(T)], uint32_t (&top)[n_freqs(T)], float& sq) {
-  constexpr int CH = q8_chunk(T);
+__device__ __forceinline__ void q8_planes(const Q8RowsArgs& a, int c0, const float (&v)[q8_chunk(T, sizeof(Elt)) * T],
+                                          float (&pl)[T][q8_chunk(T, sizeof(Elt))], uint32_t (&top)[n_freqs(T)], float& sq) {
+  constexpr int CH = q8_chunk(T, sizeof(Elt));
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     float g[T], o[T];
@@ -200,21 +218,34 @@ __device__ __forceinline__ void q8_planes(const Q8RowsArgs& a, int c0, const flo
   }
 }
 
-template <int T>
-__device__ __forceinline__ void q8_store(const Q8RowsArgs& a, int64_t row, int c0, const float (&pl)[T][q8_chunk(T)],
+template <typename Elt, int T>
+__device__ __forceinline__ void q8_store(const Q8RowsArgs& a, int64_t row, int c0, const float (&pl)[T][q8_chunk(T, sizeof(Elt))],
                                          const float (&inv)[n_freqs(T)]) {
-  constexpr int CH = q8_chunk(T), W = CH / 4;
-  if (c0 >= a.pitch) return;
-  unsigned char* out = a.codes + row * ((int64_t)a.pitch * T) + c0;
+  constexpr int CH = q8_chunk(T, sizeof(Elt)), W = CH / 4;
+  if (c0 >= a.pitch) return;  // whole quads: rows of codes are multiples of 16
+  unsigned char* out = a.codes + row * ((int64_t)a.pitch * T);
+  if constexpr (CH == 1) {
+    const int lane = (int)threadIdx.x & 3;
 #pragma unroll
-  for (int p = 0; p < T; ++p) {
-    uint32_t w[W];
+    for (int p0 = 0; p0 < T; p0 += 4) {
+      float v[4];
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = q8_encode4(pl[p][4 * i], pl[p][4 * i + 1], pl[p][4 * i + 2], pl[p][4 * i + 3], inv[freq_of(T, p)]);
-    unsigned char* q = out + p * a.pitch;
-    if constexpr (W == 4) *reinterpret_cast<u32x4*>(q) = (u32x4){w[0], w[1], w[2], w[3]};
-    else if constexpr (W == 2) *reinterpret_cast<u32x2*>(q) = (u32x2){w[0], w[1]};
-    else *reinterpret_cast<uint32_t*>(q) = w[0];
+      for (int i = 0; i < 4; ++i) v[i] = p0 + i < T ? pl[p0 + i < T ? p0 + i : 0][0] * inv[freq_of(T, p0 + i < T ? p0 + i : 0)] : 0.0f;
+      const uint32_t w = quad_transpose(q8_encode4(v[0], v[1], v[2], v[3]));
+      if (p0 + lane < T) *reinterpret_cast<uint32_t*>(out + (p0 + lane) * a.pitch + (c0 & ~3)) = w;
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < T; ++p) {
+      const float f = inv[freq_of(T, p)];
+      uint32_t w[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = q8_encode4(pl[p][4 * i] * f, pl[p][4 * i + 1] * f, pl[p][4 * i + 2] * f, pl[p][4 * i + 3] * f);
+      unsigned char* q = out + p * a.pitch + c0;
+      if constexpr (W == 4) *reinterpret_cast<u32x4*>(q) = (u32x4){w[0], w[1], w[2], w[3]};
+      else if constexpr (W == 2) *reinterpret_cast<u32x2*>(q) = (u32x2){w[0], w[1]};
+      else *reinterpret_cast<uint32_t*>(q) = w[0];
+    }
   }
 }
 
@@ -222,7 +253,7 @@ __device__ __forceinline__ void q8_store(const Q8RowsArgs& a, int64_t row, int c
 // registers between the maxima and the codes.
 template <typename Elt, int T, int LPR, int K>
 __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
-  constexpr int G = 256 / LPR, CH = q8_chunk(T), F = n_freqs(T), W = LPR / 64;
+  constexpr int G = 256 / LPR, CH = q8_chunk(T, sizeof(Elt)), F = n_freqs(T), W = LPR / 64;
   __shared__ uint32_t redTop[2][W > 1 ? F * W : 1];
   __shared__ float redSq[2][W > 1 ? W : 1];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
@@ -281,7 +312,7 @@ __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
     }
     if (live) {
 #pragma unroll
-      for (int i = 0; i < K; ++i) q8_store<T>(a, row, (lane + i * LPR) * CH, pl[i], inv);
+      for (int i = 0; i < K; ++i) q8_store<Elt, T>(a, row, (lane + i * LPR) * CH, pl[i], inv);
     }
   }
 }
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
 // cache).
 template <typename Elt, int T>
 __global__ void __launch_bounds__(256) eql_q8_rows_wide_kernel(const Q8RowsArgs a) {
-  constexpr int CH = q8_chunk(T), F = n_freqs(T);
+  constexpr int CH = q8_chunk(T, sizeof(Elt)), F = n_freqs(T);
   __shared__ uint32_t redTop[F * 4];
   __shared__ float redSq[4];
   const int64_t row = blockIdx.x;
@@ -334,7 +365,7 @@ __global__ void __launch_bounds__(256) eql_q8_rows_wide_kernel(const Q8RowsArgs 
       for (int e = 0; e < CH * T; ++e) v[e] = 0.0f;
     }
     q8_planes<Elt, T>(a, c0, v, pl, unused, none);
-    q8_store<T>(a, row, c0, pl, inv);
+    q8_store<Elt, T>(a, row, c0, pl, inv);
   }
 }
 
@@ -384,9 +415,11 @@ __global__ void __launch_bounds__(256) eql_q8_pack_kernel(const Q8PackArgs a) {
       Dft<T>::run(v, pl[c], a.tw);
     }
 #pragma unroll
-    for (int p = 0; p < T; ++p)
+    for (int p = 0; p < T; ++p) {
+      const float f = inv[freq_of(T, p)];
       *reinterpret_cast<uint32_t*>(a.codes + q8_weight_unit(o, i, p, T, a.kblocks)) =
-          q8_encode4(pl[0][p], pl[1][p], pl[2][p], pl[3][p], inv[freq_of(T, p)]);
+          q8_encode4(pl[0][p] * f, pl[1][p] * f, pl[2][p] * f, pl[3][p] * f);
+    }
   }
 }
 

@@ -40,7 +40,7 @@ Q8Kind product_kind(int64_t N, int64_t Cp, int64_t Dp, int T) {
   const Q8Tile b = q8_tile(T, true), m = q8_tile(T, false);
   if (ceil_div(N, 32 * b.mb) * ceil_div(Dp, 128 * b.nb) >= 192) return Q8Kind::kBig;
   const int64_t medium = ceil_div(N, 32 * m.mb) * ceil_div(Dp, 128 * m.nb);
-  return medium < 48 && q8_blocks(Cp) >= 4 ? Q8Kind::kSmall : Q8Kind::kMedium;
+  return medium < 48 ? Q8Kind::kSmall : Q8Kind::kMedium;
 }
 
 // Both entry points that write rows.
@@ -66,7 +66,7 @@ int write_rows(bool norm, const void* x, const void* res, const void* gamma, voi
   a.eps = eps;
   a.invR = (float)(1.0 / (double)(Cp * T));
   a.tw = host::twiddles(T);
-  const NormShape sh = q8_shape(ceil_div(Cp, q8_chunk(T)), T);
+  const NormShape sh = q8_shape(Cp, T, elt_bytes(dtype), N);
   int64_t grid = N;
   if (sh.k) grid = std::min(ceil_div(N, 256 / sh.lpr), kMaxGrid);
   else if (N > kMaxGrid) return EQL_EINVAL;

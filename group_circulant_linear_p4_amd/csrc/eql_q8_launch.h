@@ -7,14 +7,16 @@
 
 namespace eql {
 
-// Lanes per row of the row kernels and chunks per lane, for rows of `chunks` chunks; k = 0: the row
-// does not fit a workgroup's registers.
-constexpr NormShape q8_shape(int64_t chunks, int T) {
-  const int keep = q8_keep(T);
-  if (chunks <= 32 && keep >= 2) return {16, chunks <= 16 ? 1 : 2};
-  const int lpr = chunks <= 64 * (keep < 2 ? keep : 2) ? 64 : 256;
+// Lanes per row of the row kernels and chunks per lane, for N rows of C channels; k = 0: the row does not fit a
+// workgroup's registers.  Few rows take more lanes a row, one chunk each: their time is one wave's (197 rows of 96
+// channels, T = 4 fp16, the norm: 4.9 us on 16 lanes a row, 3.8 on 64).  Otherwise 32 values a lane: with 64, too few
+// waves hide the memory's latency (65536 rows of 1024 channels, T = 4 fp16: 165 us on 64 lanes a row, 139 on 256).
+constexpr NormShape q8_shape(int64_t C, int T, int elt, int64_t N) {
+  const int64_t chunks = (C + q8_chunk(T, elt) - 1) / q8_chunk(T, elt);
+  const int some = N <= 1024 ? 1 : q8_some(T, elt), keep = q8_keep(T, elt);
+  const int lpr = N > 4096 && chunks <= 16 * some ? 16 : (chunks <= 64 * some ? 64 : 256);
   const int64_t k = (chunks + lpr - 1) / lpr;
-  return {lpr, k > keep ? 0 : (k > 2 ? 4 : (int)k)};
+  return {lpr, k > keep ? 0 : (k > 4 ? 8 : (k > 2 ? 4 : (int)k))};
 }
 
 // How a product runs (eql_q8_gemm.h).

@@ -5,20 +5,26 @@
 
 namespace eql {
 
+// The lanes and chunks that q8_shape gives.
 template <typename Elt, int T>
 static const void* q8_rows_fn(NormShape sh) {
-  constexpr int KEEP = q8_keep(T);
+  constexpr int SOME = q8_some(T, sizeof(Elt)), KEEP = q8_keep(T, sizeof(Elt));
   if (sh.k == 0) return (const void*)&eql_q8_rows_wide_kernel<Elt, T>;
-  if constexpr (KEEP >= 2) {
-    if (sh.lpr == 16) return sh.k == 1 ? (const void*)&eql_q8_rows_kernel<Elt, T, 16, 1> : (const void*)&eql_q8_rows_kernel<Elt, T, 16, 2>;
-    if (sh.k == 2) return sh.lpr == 64 ? (const void*)&eql_q8_rows_kernel<Elt, T, 64, 2> : (const void*)&eql_q8_rows_kernel<Elt, T, 256, 2>;
-  }
-  if constexpr (KEEP >= 4) {
-    if (sh.k == 4) return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 4>;
-  }
   if (sh.k == 1) {
-    if (sh.lpr == 64) return (const void*)&eql_q8_rows_kernel<Elt, T, 64, 1>;
-    return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 1>;
+    if (sh.lpr == 16) return (const void*)&eql_q8_rows_kernel<Elt, T, 16, 1>;
+    return sh.lpr == 64 ? (const void*)&eql_q8_rows_kernel<Elt, T, 64, 1> : (const void*)&eql_q8_rows_kernel<Elt, T, 256, 1>;
+  }
+  if (sh.lpr == 256) {
+    if (sh.k == 2) return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 2>;
+    if (sh.k == 4) return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 4>;
+    if constexpr (KEEP == 8) return (const void*)&eql_q8_rows_kernel<Elt, T, 256, 8>;
+    return nullptr;
+  }
+  if constexpr (SOME >= 2) {
+    if (sh.k == 2) return sh.lpr == 16 ? (const void*)&eql_q8_rows_kernel<Elt, T, 16, 2> : (const void*)&eql_q8_rows_kernel<Elt, T, 64, 2>;
+  }
+  if constexpr (SOME >= 4) {
+    if (sh.k == 4) return sh.lpr == 16 ? (const void*)&eql_q8_rows_kernel<Elt, T, 16, 4> : (const void*)&eql_q8_rows_kernel<Elt, T, 64, 4>;
   }
   return nullptr;
 }

@@ -44,8 +44,8 @@ extern "C" {
  */
 size_t eqlinear_q8_rows_bytes(int64_t N, int64_t Cp, int T);
 
-/* x: [N][Cp*T] read; rows8: eqlinear_q8_rows_bytes(N, Cp, T) bytes written.  Rows that a workgroup's
- * registers do not hold (over 16384 features for T <= 4, 10240 for T <= 8, 9216 above) take N <= 2^24 - 1. */
+/* x: [N][Cp*T] read; rows8: eqlinear_q8_rows_bytes(N, Cp, T) bytes written.  Some rows over 6144 features (those
+ * that a workgroup's registers do not hold) take N <= 2^24 - 1 (EQL_EINVAL otherwise), here and below. */
 int eqlinear_q8_quantize(const void* x, void* rows8, int64_t N, int64_t Cp, int T, int dtype, void* stream);
 
 /*
