@@ -13,7 +13,9 @@ the C_4 view described in include/eqlinear.h.  With a bias,
 GELU or a residual, the forward is eqlinear_fwd_fused (eqlinear_fwd_fused_train when the
 weight needs a gradient) and the backward starts with eqlinear_fused_epilogue_bwd.  EQLayerNorm is the
 equivariant layer norm, and EQMLPBlock the pre-norm MLP block built from both, which by default
-keeps its activations for the backward in 8 bits (include/eqlinear_block.h).  Torch only allocates the buffers; every arithmetic step
+keeps its activations for the backward in 8 bits (include/eqlinear_block.h).  EQRMSNorm is the RMS norm with
+the residual's addition (include/eqlinear_rmsnorm.h).  EQLinear8bit and EQMLPBlock8bit are the inference forms of a
+layer and of a block in 8-bit integers (include/eqlinear_q8.h).  Torch only allocates the buffers; every arithmetic step
 runs in the HIP library.  The backward passes have no derivative of their own: asking for gradients
 of gradients raises.
 """
@@ -32,7 +34,9 @@ from . import (EQL_ACT_GELU, EQL_ACT_NONE, EQL_PACK_BWDX, EQL_PACK_FWD, eqlinear
                eqlinear_layernorm_bwd, eqlinear_layernorm_bwd_ckpt8, eqlinear_layernorm_bwd_workspace_bytes,
                eqlinear_layernorm_fwd,
                eqlinear_p4m_expand_weight, eqlinear_p4m_fold_weight_grad, eqlinear_pack_weight,
-               eqlinear_packed_weight_bytes)
+               eqlinear_packed_weight_bytes, eqlinear_q8_fwd, eqlinear_q8_pack_weight, eqlinear_q8_quantize,
+               eqlinear_q8_rmsnorm, eqlinear_q8_rows_bytes, eqlinear_q8_weight_bytes, eqlinear_rmsnorm_bwd,
+               eqlinear_rmsnorm_bwd_workspace_bytes, eqlinear_rmsnorm_fwd)
 
 
 def _dense(t: torch.Tensor) -> torch.Tensor:
@@ -425,6 +429,95 @@ class EQLayerNorm(torch.nn.Module):
         return "channels=%d, group_order=%d, eps=%g, ckpt8=%s" % (self.channels, self.group_order, self.eps, self.ckpt8)
 
 
+class EQRMSNormFunction(torch.autograd.Function):
+    """y = weight s / rms(s) of rows of C'*T features, one weight per channel, shared by its T group
+    elements, for s = x + residual (include/eqlinear_rmsnorm.h).  Returns y, or (y, s) with a residual.
+    Kept for the backward: s and the rows' 1 / rms."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, residual, gamma, T: int, eps: float, grad_mode: bool):
+        N, Cp = _norm_operands(x, residual, gamma, T)
+        R = Cp * T
+        x2 = _rows(x, R)
+        r2 = _rows(residual, R) if residual is not None else None
+        gamma = gamma.contiguous() if gamma is not None else None
+        y = torch.empty_like(x2)
+        s = torch.empty_like(x2) if residual is not None else None
+        train = grad_mode and any(ctx.needs_input_grad[:3])
+        rstd = torch.empty(N, dtype=torch.float32, device=x.device) if train else None
+        eqlinear_rmsnorm_fwd(x2, r2, gamma, s, y, rstd, N, Cp, T, eps, x.dtype)
+        ctx.set_materialize_grads(False)
+        ctx.sizes, ctx.dtype, ctx.shape = (N, Cp, T), x.dtype, x.shape
+        if s is None:
+            ctx.save_for_backward(x2 if train else None, rstd, gamma)
+            return y.reshape(x.shape)
+        s = s.reshape(x.shape)
+        ctx.save_for_backward(s if train else None, rstd, gamma)
+        return y.reshape(x.shape), s
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, rstd, gamma = ctx.saved_tensors
+        N, Cp, T = ctx.sizes
+        R = Cp * T
+        need_x, need_r, need_g = ctx.needs_input_grad[:3]
+        if dy is None:  # only the sum was used
+            if ds is None:
+                return None, None, None, None, None, None
+            dg = torch.zeros_like(gamma) if need_g else None
+            return ds if need_x else None, ds if need_r else None, dg, None, None, None
+        dy2 = _rows(dy.to(ctx.dtype), R)
+        ds2 = _rows(ds.to(ctx.dtype), R) if ds is not None else None
+        dx = torch.empty_like(dy2)
+        dg = torch.empty(Cp, dtype=ctx.dtype, device=dy2.device) if need_g else None
+        n = eqlinear_rmsnorm_bwd_workspace_bytes(N, Cp, T, ctx.dtype)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dy2.device)
+        eqlinear_rmsnorm_bwd(dy2, _rows(s, R), rstd, gamma, ds2, dx, dg, ws, n, N, Cp, T, ctx.dtype)
+        dx = dx.reshape(ctx.shape)
+        return dx if need_x else None, dx if need_r else None, dg, None, None, None
+
+
+def _norm_operands(x, residual, gamma, T):
+    """(rows, channels) of a norm's input after the checks that its kernels rely on."""
+    R = x.shape[-1]
+    if T < 1 or R % T != 0:
+        raise ValueError("x has %d features, not a multiple of the group order %d" % (R, T))
+    Cp = R // T
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.device != x.device):
+        raise ValueError("residual must have x's shape, dtype and device")
+    if gamma is not None:
+        if gamma.dim() != 1 or gamma.numel() != Cp:
+            raise ValueError("weight must be 1-D with C' = %d values (one per channel, shared over the group), got "
+                             "shape %s" % (Cp, tuple(gamma.shape)))
+        if gamma.dtype != x.dtype or gamma.device != x.device:
+            raise ValueError("x and weight must share a dtype (fp16 or fp32) and a device")
+    return x.numel() // R if R else 0, Cp
+
+
+def eq_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, group_order: int = 1, eps: float = 1e-6,
+                residual: torch.Tensor | None = None):
+    """RMS norm over the last axis (C'*T features), weight [C'].  With a residual, the norm of s = x + residual
+    (rounded to x's dtype): returns (y, s).  Differentiable in x, residual and weight."""
+    return EQRMSNormFunction.apply(x, residual, weight, group_order, eps, torch.is_grad_enabled())
+
+
+class EQRMSNorm(torch.nn.Module):
+    """Equivariant RMS norm over channels * T features: one weight per channel.  Called with a residual it
+    adds it first and returns (norm, sum)."""
+
+    def __init__(self, channels: int, group_order: int = 4, eps: float = 1e-6, device=None, dtype=None):
+        super().__init__()
+        self.channels, self.group_order, self.eps = channels, group_order, eps
+        self.weight = torch.nn.Parameter(torch.ones(channels, device=device, dtype=dtype))
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        return eq_rms_norm(x, self.weight, self.group_order, self.eps, residual)
+
+    def extra_repr(self) -> str:
+        return "channels=%d, group_order=%d, eps=%g" % (self.channels, self.group_order, self.eps)
+
+
 class EQMLPBlock8bitFunction(torch.autograd.Function):
     """y = x + W2 gelu(W1 norm(x) + b1) + b2 keeping, from the forward to the backward, the
     normalised rows and GELU's input as 8-bit checkpoints and nothing else of their size.
@@ -534,13 +627,16 @@ class EQMLPBlock(torch.nn.Module):
     fp32) and as much again for the kept spectra when it is off; the gradients are those of the
     rounded activations (each within 1/127 of its block's largest).  The block then reads its
     submodules' parameters; where a submodule was replaced, hooked or set to compute something else,
-    it calls them one after the other, as without ckpt8."""
+    it calls them one after the other, as without ckpt8.  norm: "layer", or "rms" for EQRMSNorm (whose
+    block keeps its activations as they are, as without ckpt8)."""
 
     def __init__(self, channels: int, hidden_channels: int, group_order: int = 4, eps: float = 1e-5, device=None,
-                 dtype=None, ckpt8: bool = True):
+                 dtype=None, ckpt8: bool = True, norm: str = "layer"):
         super().__init__()
-        self.ckpt8 = ckpt8
-        self.norm = EQLayerNorm(channels, group_order, eps, device=device, dtype=dtype)
+        if norm not in ("layer", "rms"):
+            raise ValueError("norm must be 'layer' or 'rms'")
+        self.ckpt8 = ckpt8 and norm == "layer"
+        self.norm = (EQLayerNorm if norm == "layer" else EQRMSNorm)(channels, group_order, eps, device=device, dtype=dtype)
         self.fc1 = EQLinear(channels, hidden_channels, group_order, bias=True, activation="gelu", device=device, dtype=dtype)
         self.fc2 = EQLinear(hidden_channels, channels, group_order, bias=True, device=device, dtype=dtype)
 
@@ -561,3 +657,152 @@ class EQMLPBlock(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return "ckpt8=%s" % self.ckpt8
+
+
+class EQRows8:
+    """Rows in 8 bits: what eqlinear_q8_quantize and eqlinear_q8_rmsnorm write, with the sizes to read it by."""
+
+    __slots__ = ("data", "lead_shape", "channels", "group_order", "dtype")
+
+    def __init__(self, data: torch.Tensor, lead_shape, channels: int, group_order: int, dtype: torch.dtype):
+        self.data, self.lead_shape, self.channels, self.group_order, self.dtype = data, lead_shape, channels, group_order, dtype
+
+
+def _inference(*tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError("the 8-bit layers are inference forms without a backward pass: call them under "
+                           "torch.no_grad() or on tensors that need no gradient")
+
+
+def eq_quantize_8bit(x: torch.Tensor, group_order: int = 1) -> EQRows8:
+    """x [..., C'*T] as 8-bit rows (a scale for each row and frequency)."""
+    _inference(x)
+    N, Cp = _norm_operands(x, None, None, group_order)
+    data = torch.empty(max(eqlinear_q8_rows_bytes(N, Cp, group_order), 16), dtype=torch.uint8, device=x.device)
+    eqlinear_q8_quantize(_rows(x, x.shape[-1]), data, N, Cp, group_order, x.dtype)
+    return EQRows8(data, x.shape[:-1], Cp, group_order, x.dtype)
+
+
+def eq_rms_norm_8bit(x: torch.Tensor, weight: torch.Tensor | None = None, group_order: int = 1, eps: float = 1e-6,
+                     residual: torch.Tensor | None = None):
+    """eq_rms_norm with its output as 8-bit rows: returns them, or (rows, x + residual)."""
+    _inference(x, weight, residual)
+    N, Cp = _norm_operands(x, residual, weight, group_order)
+    R = x.shape[-1]
+    data = torch.empty(max(eqlinear_q8_rows_bytes(N, Cp, group_order), 16), dtype=torch.uint8, device=x.device)
+    s = torch.empty((N, R), dtype=x.dtype, device=x.device) if residual is not None else None
+    eqlinear_q8_rmsnorm(_rows(x, R), _rows(residual, R) if residual is not None else None,
+                        weight.contiguous() if weight is not None else None, s, data, N, Cp, group_order, eps, x.dtype)
+    rows = EQRows8(data, x.shape[:-1], Cp, group_order, x.dtype)
+    return rows if s is None else (rows, s.reshape(x.shape))
+
+
+class EQLinear8bit(torch.nn.Module):
+    """Inference form of EQLinear in 8-bit integers: the weight's half spectrum with a scale for each output
+    channel and frequency, packed once; activations quantised as they come, or given as EQRows8.  Made by
+    from_float, from an EQLinear or an EQLinearP4M (as the layer over C_4 on twice the channels that it runs as).
+    Its outputs are those of the rounded layer, about 1% of their norm off the exact one."""
+
+    def __init__(self, in_channels: int, out_channels: int, group_order: int, bias: bool = False,
+                 activation: str | None = None, device=None, dtype=None):
+        super().__init__()
+        _act_code(activation)
+        self.in_channels, self.out_channels, self.group_order = in_channels, out_channels, group_order
+        self.activation = activation
+        n = eqlinear_q8_weight_bytes(out_channels, in_channels, group_order)
+        if n == 0:
+            raise ValueError("no 8-bit weight of %d x %d channels over C_%d" % (out_channels, in_channels, group_order))
+        # Zeros: a layer of zero weights until a weight is packed or loaded.
+        self.register_buffer("weight8", torch.zeros(n, dtype=torch.uint8, device=device))
+        self.register_buffer("bias", torch.zeros(out_channels, device=device, dtype=dtype) if bias else None)
+
+    @classmethod
+    @torch.no_grad()
+    def from_float(cls, layer: torch.nn.Module) -> "EQLinear8bit":
+        w, bias, act = layer.weight.detach(), getattr(layer, "bias", None), getattr(layer, "activation", None)
+        if isinstance(layer, EQLinearP4M):
+            Dp, Cp, _ = w.shape
+            w4 = torch.empty((2 * Dp, 2 * Cp, 4), dtype=w.dtype, device=w.device)
+            eqlinear_p4m_expand_weight(_dense(w), w4, Dp, Cp, w.dtype)
+            w = w4
+        elif not isinstance(layer, EQLinear):
+            raise TypeError("expected an EQLinear or an EQLinearP4M, got %s" % type(layer).__name__)
+        Dp, Cp, T = w.shape
+        made = cls(Cp, Dp, T, bias is not None, act, device=w.device, dtype=w.dtype)
+        made.pack(w)
+        if bias is not None:
+            made.bias.copy_(bias)
+        return made
+
+    @torch.no_grad()
+    def pack(self, w: torch.Tensor) -> None:
+        """Packs a weight [D', C', T]."""
+        if tuple(w.shape) != (self.out_channels, self.in_channels, self.group_order):
+            raise ValueError("expected a weight of shape %s, got %s" % (
+                (self.out_channels, self.in_channels, self.group_order), tuple(w.shape)))
+        if w.device != self.weight8.device:
+            raise ValueError("the weight must be on the layer's device (%s), got %s" % (self.weight8.device, w.device))
+        eqlinear_q8_pack_weight(_dense(w), self.weight8, self.out_channels, self.in_channels, self.group_order, w.dtype)
+
+    def forward(self, x, residual: torch.Tensor | None = None) -> torch.Tensor:
+        """y = act(x W^T + bias) + residual; x: a tensor [..., C'*T] or EQRows8."""
+        Dp, Cp, T = self.out_channels, self.in_channels, self.group_order
+        _inference(residual)
+        if not isinstance(x, EQRows8):
+            if x.shape[-1] != Cp * T:
+                raise ValueError("x has %d features, the weight expects C'*T = %d" % (x.shape[-1], Cp * T))
+            if x.device != self.weight8.device:
+                raise ValueError("x must be on the layer's device (%s), got %s" % (self.weight8.device, x.device))
+            x = eq_quantize_8bit(x, T)
+        if (x.channels, x.group_order) != (Cp, T) or x.data.device != self.weight8.device:
+            raise ValueError("the rows have %d channels over C_%d on %s, the layer %d over C_%d on %s" % (
+                x.channels, x.group_order, x.data.device, Cp, T, self.weight8.device))
+        shape = (*x.lead_shape, Dp * T)
+        if self.bias is not None and self.bias.dtype != x.dtype:
+            raise ValueError("x and bias must share a dtype (fp16 or fp32)")
+        if residual is not None and (residual.shape != shape or residual.dtype != x.dtype or residual.device != x.data.device):
+            raise ValueError("residual must have the output's shape, dtype and device")
+        N = math.prod(x.lead_shape)
+        y = torch.empty((N, Dp * T), dtype=x.dtype, device=x.data.device)
+        eqlinear_q8_fwd(x.data, self.weight8, self.bias, _rows(residual, Dp * T) if residual is not None else None, y,
+                        N, Cp, Dp, T, x.dtype, _act_code(self.activation))
+        return y.reshape(shape)
+
+    def extra_repr(self) -> str:
+        return "in_channels=%d, out_channels=%d, group_order=%d, bias=%s, activation=%s" % (
+            self.in_channels, self.out_channels, self.group_order, self.bias is not None, self.activation)
+
+
+class EQMLPBlock8bit(torch.nn.Module):
+    """Inference form of EQMLPBlock with its two layers in 8-bit integers.  With an RMS norm, the norm writes the
+    first layer's 8-bit rows itself; called with a residual (RMS norm only), the block is of x + residual, added in
+    the norm's pass."""
+
+    def __init__(self, norm: torch.nn.Module, fc1: EQLinear8bit, fc2: EQLinear8bit):
+        super().__init__()
+        self.norm, self.fc1, self.fc2 = norm, fc1, fc2
+
+    @classmethod
+    def from_float(cls, block: EQMLPBlock) -> "EQMLPBlock8bit":
+        """The norm is the block's own; the layers are packed anew."""
+        return cls(block.norm, EQLinear8bit.from_float(block.fc1), EQLinear8bit.from_float(block.fc2))
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
+        _inference(x, residual)
+        with torch.no_grad():
+            return self._forward(x, residual)
+
+    def _forward(self, x: torch.Tensor, residual) -> torch.Tensor:
+        n = self.norm
+        if _as_made(n, EQRMSNorm) and not torch.nn.modules.module._has_any_global_hook():
+            rows = eq_rms_norm_8bit(x, n.weight, n.group_order, n.eps, residual)
+            if residual is not None:
+                rows, x = rows
+            return self.fc2(self.fc1(rows), residual=x)
+        if residual is not None:
+            if not isinstance(n, EQRMSNorm):
+                raise ValueError("only a block with an RMS norm takes a residual")
+            u, x = n(x, residual)
+        else:
+            u = n(x)
+        return self.fc2(self.fc1(u), residual=x)
