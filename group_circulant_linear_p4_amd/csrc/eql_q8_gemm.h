@@ -43,6 +43,21 @@ __device__ __forceinline__ u32x4 q8_neg(const u32x4& v) {
 
 #endif
 
+// GELU in its exact form, v Phi(v) = max(v, 0) - |v| (1 - Phi(|v|)), with 1 - Phi(a) = 2^p(a): p is a polynomial of
+// degree 5 with p(0) = -1, fitted to log2(1 - Phi) for the least largest error of the product a (1 - Phi(a)), 5.4e-7
+// (7.2e-7 in fp32 arithmetic over the whole range; p falls without end, so the tail goes to zero).  One transcendental
+// operation and eight others where gelu_erf has two and 13: a product's epilogue is bound by them.  The bound on |v|
+// keeps infinity times zero out; a NaN stays one.
+__device__ __forceinline__ float gelu_power(float v) {
+  const float a = __builtin_fabsf(v);
+  float q = __builtin_fmaf(-4.881021735e-4f, a, 7.198718573e-3f);
+  q = __builtin_fmaf(q, a, -5.214663193e-2f);
+  q = __builtin_fmaf(q, a, -0.4595958445f);
+  q = __builtin_fmaf(q, a, -1.151000542f);
+  q = __builtin_fmaf(q, a, -1.0f);
+  return __builtin_fmaf(-__builtin_fminf(a, 1e30f), __builtin_amdgcn_exp2f(q), __builtin_fmaxf(v, 0.0f));
+}
+
 #if defined(__HIP_DEVICE_COMPILE__)
 // The T outputs of one (row, output channel) before the activation: scaled planes, inverse transform,
 // bias.  sum * (scale of the channel * scale of the row) in one fused operation each where the transform's
@@ -84,7 +99,7 @@ __device__ __forceinline__ void q8_finish(const Q8FwdArgs& a, const int32_t (&su
   float y[T];
   q8_outputs<T>(sum, scale, bias, y, a.f.tw);
 #pragma unroll
-  for (int g = 0; g < T; ++g) y[g] = (a.f.act == 1 ? gelu_erf(y[g]) : y[g]) + res[g];
+  for (int g = 0; g < T; ++g) y[g] = (a.f.act == 1 ? gelu_power(y[g]) : y[g]) + res[g];
   store_group<T, Elt>(static_cast<Elt*>(a.f.y) + at, y);
 #endif
 }
@@ -271,8 +286,9 @@ __global__ void __launch_bounds__(T <= 8 ? 512 : 256) eql_q8_small_kernel(const 
 #endif
 }
 
-// Many rows: a workgroup takes a tile of 32 MB WM rows x 32 NB (4 / WM) output channels of all planes, its
-// four waves WM down and 4 / WM across, MB x NB blocks of 32 x 32 each.
+// Many rows: a workgroup takes a tile of 32 MB rows x 128 NB output channels of all planes, its four waves side by
+// side, MB x NB blocks of 32 x 32 each (two waves down and two across read the rows' LDS half as often and the weight
+// twice: no faster).
 //   * Rows' codes go through an LDS ring of four slots, a K block (64 input channels of every plane) each, by
 //     loads that write LDS directly (1 KB: 16 rows x 64 bytes of a plane), three blocks ahead.  Piece q (16
 //     bytes) of row r lies at place q ^ (r / 4) % 4 of its 64 bytes, so the 16 rows that a fragment read takes
@@ -284,11 +300,11 @@ __global__ void __launch_bounds__(T <= 8 ? 512 : 256) eql_q8_small_kernel(const 
 //   * A block is 2 MB groups (a step of 32 input channels, 32 rows) of products.  Each plane of the next
 //     group's rows is read from LDS as soon as this group's products of the plane have been issued; at the last
 //     group from the next slot, so the wait for its loads and the barrier come before that group's products.
-template <int T, typename Elt, int MB, int NB, int WM>
+template <int T, typename Elt, int MB, int NB>
 __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_kernel(const Q8FwdArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NR = n_real_planes(T), NP = n_pairs(T), F = n_freqs(T);
-  constexpr int BM = 32 * MB * WM, WN = 4 / WM, NS = 4;
+  constexpr int BM = 32 * MB, NS = 4;
   constexpr int CHUNKS = T * BM / 16;              // 1 KB loads of a slot
   constexpr int PER = (CHUNKS + 3) / 4;            // of a wave (where four do not divide them, some twice)
   constexpr int SLOT = CHUNKS * 64;                // 16-byte pieces
@@ -315,9 +331,8 @@ __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_
   const int row0 = rowTile * BM;
   const int rows = min(BM, a.f.N - row0);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wm = wave % WM, wn = wave / WM;
   const int lane = (int)threadIdx.x & 63, lrow = lane & 31;
-  const int block0 = (colTile * WN + wn) * NB;     // this wave's first block of 32 output channels
+  const int block0 = (colTile * 4 + wave) * NB;     // this wave's first block of 32 output channels
   const int nblk = a.Dpad / 32;
   const uint32_t rowBytes = (uint32_t)a.pitch * T;
   const uint32_t blockBytes = (uint32_t)T * 2048u;
@@ -376,7 +391,7 @@ __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_
 
   u32x4 xa[T];
   auto read_row = [&](const u32x4* slot, int s, int mb, int p) __attribute__((always_inline)) {
-    const int r = (wm * MB + mb) * 32 + lrow;
+    const int r = mb * 32 + lrow;
     const int q = (s * 2 + (lane >> 5)) ^ ((r >> 2) & 3);
     xa[p] = slot[p * (BM * 4) + r * 4 + q];
   };
@@ -447,17 +462,16 @@ __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_
 
   // Epilogue in chunks of CH rows: outputs past the rows or channels get an offset beyond the descriptor's
   // range.  A chunk's residual is loaded while the one before is finished (and before the chunk's own stores:
-  // it may be y); without one its range is empty.
+  // it may be y).
   constexpr int ELT = (int)sizeof(Elt);
   constexpr int RW = group_words<T, Elt>(), CH = T > 8 ? 1 : (RW <= 2 ? 16 : (RW <= 4 ? 8 : 4)), PARTS = 16 / CH;
   const uint32_t outRow = (uint32_t)a.f.Dout * T * ELT;
   const __amdgpu_buffer_rsrc_t yr = make_rsrc(static_cast<char*>(a.f.y) + (size_t)row0 * outRow, (uint32_t)rows * outRow);
-  const __amdgpu_buffer_rsrc_t rr =
-      make_rsrc(static_cast<const char*>(a.f.res) + (size_t)row0 * outRow, a.f.res ? (uint32_t)rows * outRow : 0u);
+  const __amdgpu_buffer_rsrc_t rr = make_rsrc(static_cast<const char*>(a.f.res) + (size_t)row0 * outRow, (uint32_t)rows * outRow);
   constexpr bool EARLY = T * MB * NB <= 4 && CH * RW <= 32;
   uint32_t res[2][CH][RW];
   auto offset_of = [&](int nb, int mb, int r) __attribute__((always_inline)) {
-    const int col = (block0 + nb) * 32 + lrow, row = (wm * MB + mb) * 32 + 4 * (lane >> 5);
+    const int col = (block0 + nb) * 32 + lrow, row = mb * 32 + 4 * (lane >> 5);
     const uint32_t off = col < a.f.Dout ? (uint32_t)row * outRow + (uint32_t)(col * T * ELT) : kOob;
     return off + (uint32_t)(8 * (r >> 2) + (r & 3)) * outRow;
   };
@@ -479,7 +493,8 @@ __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_
     for (int f = 0; f < F; ++f) ws[nb][f] = a.wScales[(int64_t)f * a.Dpad + min(col, a.Dpad - 1)];
     bias[nb] = a.f.bias ? (float)static_cast<const Elt*>(a.f.bias)[min(col, a.f.Dout - 1)] : 0.0f;
   }
-  if constexpr (EARLY) load_res(0);
+  if constexpr (EARLY)
+    if (a.f.res) load_res(0);
   __builtin_amdgcn_sched_barrier(0);
   issue_rows(0, ring0, 0, PER);
   __builtin_amdgcn_sched_barrier(0);
@@ -505,36 +520,44 @@ __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_
     if (++kb >= a.kblocks) break;
   }
 
-  auto finish = [&](auto geluTag) __attribute__((always_inline)) {
-    constexpr bool GELU = decltype(geluTag)::value;
+  auto finish = [&](auto geluTag, auto resTag) __attribute__((always_inline)) {
+    constexpr bool GELU = decltype(geluTag)::value, RES = decltype(resTag)::value;
 #pragma unroll
     for (int i = 0; i < NB * MB * PARTS; ++i) {
       const int nb = i / PARTS / MB, mb = i / PARTS % MB, c = i % PARTS * CH;
-      if (i + 1 < NB * MB * PARTS) load_res(i + 1);
+      if (RES && i + 1 < NB * MB * PARTS) load_res(i + 1);
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        const int r = c + j, row = (wm * MB + mb) * 32 + 4 * (lane >> 5) + 8 * (r >> 2) + (r & 3);
+        const int r = c + j, row = mb * 32 + 4 * (lane >> 5) + 8 * (r >> 2) + (r & 3);
         int32_t sum[T];
-        float scale[F], y[T], v[T];
+        float scale[F], y[T], v[T] = {};
 #pragma unroll
         for (int p = 0; p < T; ++p) sum[p] = acc[mb][nb][p][r];
 #pragma unroll
         for (int f = 0; f < F; ++f) scale[f] = ws[nb][f] * rowScale[row * F + f];
         q8_outputs<T>(sum, scale, bias[nb], y, a.f.tw);
-        group_from_raw<T, Elt>(res[i & 1][j], v);
+        if constexpr (RES) group_from_raw<T, Elt>(res[i & 1][j], v);
 #pragma unroll
-        for (int g = 0; g < T; ++g) y[g] = (GELU ? gelu_erf(y[g]) : y[g]) + v[g];
+        for (int g = 0; g < T; ++g) y[g] = (GELU ? gelu_power(y[g]) : y[g]) + (RES ? v[g] : 0.0f);
         store_group_buf<T, Elt>(yr, offset_of(nb, mb, r), y);
         // A few rows at a time: all interleaved, their sums leave the accumulators together and spill.
         if (T > 8 || (j & 3) == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
-  // No load into LDS outlives the workgroup: the residuals' wait covers the older loads.
-  if constexpr (EARLY) wait_vmcnt<0>();
-  else load_res(0);
-  if (a.f.act == 1) finish(std::true_type{});
-  else finish(std::false_type{});
+  // No load into LDS outlives the workgroup: a later residual's wait covers the older loads.
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (a.f.res) {
+    if constexpr (EARLY) wait_vmcnt<0>();
+    else load_res(0);
+    if (a.f.act == 1) finish(Yes{}, Yes{});
+    else finish(No{}, Yes{});
+  } else {
+    wait_vmcnt<0>();
+    if (a.f.act == 1) finish(Yes{}, No{});
+    else finish(No{}, No{});
+  }
 #endif
 }
 

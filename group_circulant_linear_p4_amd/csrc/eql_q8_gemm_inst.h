@@ -11,8 +11,8 @@ static hipError_t q8_fwd_one(Q8Kind kind, const Q8FwdArgs& a, unsigned grid, hip
   if (kind == Q8Kind::kToken) return launch_kernel((const void*)&eql_q8_token_kernel<T, Elt>, grid, a, s);
   if (kind == Q8Kind::kSmall) return launch_kernel((const void*)&eql_q8_small_kernel<T, Elt>, grid, a, s, 64u * (unsigned)a.waves);
   if constexpr (T <= kQ8LargeT) {
-    if (kind == Q8Kind::kBig) return launch_kernel((const void*)&eql_q8_large_kernel<T, Elt, B.mb, B.nb, 1>, grid, a, s);
-    return launch_kernel((const void*)&eql_q8_large_kernel<T, Elt, M.mb, M.nb, 1>, grid, a, s);
+    if (kind == Q8Kind::kBig) return launch_kernel((const void*)&eql_q8_large_kernel<T, Elt, B.mb, B.nb>, grid, a, s);
+    return launch_kernel((const void*)&eql_q8_large_kernel<T, Elt, M.mb, M.nb>, grid, a, s);
   }
   return hipErrorInvalidValue;
 }
