@@ -145,7 +145,7 @@ int eqlinear_q8_fwd(const void* rows8, const void* w8, const void* bias, const v
   const int64_t rowTiles = token ? 1 : ceil_div(N, small ? 32 : 32 * tile.mb);
   const int64_t colTiles = ceil_div(Dp, token ? 8 : (small ? 32 : 128 * tile.nb));
   const int64_t grid = rowTiles * colTiles;
-  if (grid > kMaxGrid / 2) return EQL_EINVAL;
+  if (grid > kMaxGrid) return EQL_EINVAL;  // 512 threads only in grids of up to 256
   a.colTiles = (int)colTiles;
   // Eight waves a tile while there is a compute unit for each (32 rows of 1024 -> 1024 channels: 5.9 us, with four 6.2),
   // else four (300 rows: 15.8 and 13.7).

@@ -67,7 +67,8 @@ int eqlinear_q8_pack_weight(const void* w, void* w8, int64_t Dp, int64_t Cp, int
  * y[n][d*T+g] = act(layer + bias[d]) + residual, the epilogue in fp32 and rounded once.
  * rows8, w8: as written by the calls above for these sizes.  bias: [Dp] of `dtype`, or NULL, aligned to
  * the element; act: EQL_ACT_NONE or EQL_ACT_GELU (any other value is EQL_EINVAL); residual: [N][Dp*T], or NULL,
- * may be y.  y: [N][Dp*T] written.
+ * may be y.  y: [N][Dp*T] written.  N and Dp that take 2^24 workgroups or more (each at least 32 rows by 32
+ * channels) are EQL_EINVAL.
  */
 int eqlinear_q8_fwd(const void* rows8, const void* w8, const void* bias, const void* residual, void* y, int64_t N,
                     int64_t Cp, int64_t Dp, int T, int dtype, int act, void* stream);
