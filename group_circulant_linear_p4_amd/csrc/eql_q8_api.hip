@@ -29,18 +29,23 @@ int check(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
 size_t row_codes(int64_t N, int64_t Cp, int T) { return (size_t)N * (size_t)T * (size_t)q8_pitch(Cp); }
 size_t weight_codes(int64_t Dp, int64_t Cp, int T) { return (size_t)(q8_out(Dp) / 32 * q8_blocks(Cp)) * (size_t)T * 2048; }
 
-// Which kernel a product takes.  The big tile reads the operands least, once it has a tile for most compute units
-// (p4 fp16 with residual, 65536 rows of 256 -> 1024 channels: 275 us against the medium tile's 322; 12608 rows of 384
-// -> 96, 197 tiles: 10.8 and 11.9; 1000 rows of 384 -> 384, 48 tiles: 9.1 and 7.0).  The small kernel splits the input
-// channels instead, where few medium tiles would each walk many of them (32 rows of 1024 -> 1024, 8 tiles: 5.9 us and
-// 10.6; 300 rows, 80 tiles: 13.7 and 12.1).
+// Which kernel a product takes (fp16, rows of input -> output channels).  The small one splits the input channels of each
+// of its 32 x 32 tiles over eight waves and is the shorter while every tile has a compute unit: T = 4, 256 rows of 1024
+// -> 1024, 256 tiles: 8.5 us and the medium tile's 10.7, of 4096 -> 1024: 24.7 and 33.5; 500 rows, 512 tiles: 14.0 and
+// 11.1.  T = 1, 500 rows of 4096 -> 1024, 512 tiles: 12.1 and 17.7; 1000 rows, 1024 tiles: 21.9 and 18.8.
+// The big tile reads the operands least, once it has a tile for most compute units: T = 4, 12608 rows of 384 -> 96, 197
+// tiles: 10.8 us and the medium one's 11.9; 1000 rows of 1024 -> 1024, 128 tiles: 15.0 and 12.2.  For T <= 2 it is 256
+// channels wide instead of 128 and four workgroups of the medium one share a compute unit, so it needs long sums or many
+// tiles (T = 1, 256 tiles of 1024 -> 1024: 11.6 us and 13.6, of 256 -> 1024: 8.5 and 7.4, 2048 of these: 38.1 and 43.9)
+// and few channels past the last one (T = 2, 65536 rows of 384 -> 384: 53.5 and 44.5).
 Q8Kind product_kind(int64_t N, int64_t Cp, int64_t Dp, int T) {
   if (N <= kQ8Tokens) return Q8Kind::kToken;
-  if (T > kQ8LargeT) return Q8Kind::kSmall;
-  const Q8Tile b = q8_tile(T, true), m = q8_tile(T, false);
-  if (ceil_div(N, 32 * b.mb) * ceil_div(Dp, 128 * b.nb) >= 192) return Q8Kind::kBig;
-  const int64_t medium = ceil_div(N, 32 * m.mb) * ceil_div(Dp, 128 * m.nb);
-  return medium < 48 ? Q8Kind::kSmall : Q8Kind::kMedium;
+  if (T > kQ8LargeT || ceil_div(N, 32) * ceil_div(Dp, 32) <= (T == 1 ? 512 : 256)) return Q8Kind::kSmall;
+  const Q8Tile b = q8_tile(T, true);
+  const int64_t tiles = ceil_div(N, 32 * b.mb) * ceil_div(Dp, 128 * b.nb);
+  if (T > 2) return tiles >= 192 ? Q8Kind::kBig : Q8Kind::kMedium;
+  const bool filled = ceil_div(Dp, 128) % 2 == 0 || Dp > 1024;
+  return filled && tiles >= (q8_blocks(Cp) >= 8 ? 256 : 1024) ? Q8Kind::kBig : Q8Kind::kMedium;
 }
 
 // Both entry points that write rows.

@@ -40,7 +40,9 @@ PRODUCTS = [(1, 1, 1, 1), (1, 64, 32, 1), (5, 65, 33, 1), (33, 200, 100, 1), (1,
 # Enough tiles for the large kernel, ragged in every axis.
 LARGE = [(1500, 70, 1050, 1), (1000, 130, 2100, 2), (1100, 65, 1700, 3), (1030, 100, 1999, 4), (2060, 64, 513, 5),
          (1030, 33, 1100, 6), (530, 130, 2048, 7), (700, 129, 1500, 8), (300, 65, 1700, 9), (300, 40, 1700, 10),
-         (290, 64, 1700, 12), (513, 20, 1000, 15), (260, 66, 2100, 16), (16500, 96, 96, 4), (4100, 20, 40, 8)]
+         (290, 64, 1700, 12), (513, 20, 1000, 15), (260, 66, 2100, 16), (16500, 96, 96, 4), (4100, 20, 40, 8),
+         # Both tiles of the large kernel, and odd and even numbers of K blocks.
+         (4200, 450, 1810, 1), (2060, 470, 2020, 2), (500, 70, 1000, 3), (500, 200, 1000, 4), (1100, 290, 1700, 4)]
 
 
 def dev(a):
