@@ -50,6 +50,14 @@ __device__ __forceinline__ float q8_top(uint32_t bits) {
 // 127 / m as the codes are defined: the reciprocal and the product each rounded.
 __device__ __forceinline__ float q8_inv(float m) { return 127.0f * (1.0f / m); }
 
+// m / 127 rounded to nearest: the quotient by the rounded 1 / 127, and one correction (all 2^23 mantissas agree with the
+// division, which takes 11 operations).
+__device__ __forceinline__ float q8_scale(float m) {
+  constexpr float inv = 1.0f / 127.0f;
+  const float q = m * inv;
+  return __builtin_fmaf(__builtin_fmaf(-127.0f, q, m), inv, q);
+}
+
 // Four codes as a word, of values times their 127 / m.  The product is rounded to fp32, then adding 1.5 2^23 rounds it
 // to an integer (ties to even), which is in the sum's low bits.  With inv a NaN the codes are not
 // specified (their scale is NaN).
@@ -71,7 +79,23 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t w) {
   return __builtin_amdgcn_perm(q, w, i & 2 ? 0x03020706u : 0x05040100u);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+// Each frequency's largest magnitude: the largest of the positive values' bits and of the negative ones' (a NaN's
+// is above infinity's).  As signed and unsigned integers the instruction that takes three operands does both without
+// the mask: an operation a value instead of two.
+template <int F>
+struct Q8Top {
+  int32_t pos[F];
+  uint32_t neg[F];
+  __device__ __forceinline__ Q8Top() {
+#pragma unroll
+    for (int f = 0; f < F; ++f) pos[f] = 0, neg[f] = 0;
+  }
+  __device__ __forceinline__ void take(int f, float v) {
+    pos[f] = max(pos[f], __builtin_bit_cast(int32_t, v));
+    neg[f] = max(neg[f], __builtin_bit_cast(uint32_t, v));
+  }
+  __device__ __forceinline__ uint32_t bits(int f) const { return max((uint32_t)pos[f], neg[f] & 0x7FFFFFFFu); }
+};
 
 // Largest of the LPR lanes of a row (LPR <= 64), on every lane.
 template <int LPR>
@@ -121,22 +145,46 @@ __host__ __device__ constexpr int q8_some(int T, int elt) {
   return n >= 4 ? 4 : (n >= 2 ? 2 : 1);
 }
 
-// The E elements at p (at element alignment) to floats, and back: pieces of 16 bytes, then 4, 2 and 1.
+// E elements as they lie in memory.
+template <typename Elt, int E>
+constexpr int q8_words() {
+  return (E * (int)sizeof(Elt) + 3) / 4;
+}
+// The E elements at p (at element alignment), or its first n where a chunk may have a TAIL: pieces of 16 bytes, then 8, 4 and 2.
 template <typename Elt, int E, int FROM = 0>
-__device__ __forceinline__ void load_elts(const Elt* p, float (&v)[E]) {
-  constexpr int N = E - FROM >= 8 && sizeof(Elt) == 2 ? 8 : (E - FROM >= 4 ? 4 : (E - FROM >= 2 ? 2 : 1));
-  if constexpr (E - FROM > 0) {
-    if constexpr (N == 1) {
-      v[FROM] = (float)p[FROM];
-    } else {
-      typedef Elt EN __attribute__((ext_vector_type(N), aligned(sizeof(Elt))));
-      const EN u = *reinterpret_cast<const EN*>(p + FROM);
+__device__ __forceinline__ void load_words(const Elt* p, uint32_t (&w)[q8_words<Elt, E>()]) {
+  constexpr int LEFT = E * (int)sizeof(Elt) - FROM * 4, N = LEFT >= 16 ? 4 : (LEFT >= 8 ? 2 : 1);
+  if constexpr (LEFT >= 4) {
+    typedef uint32_t UN __attribute__((ext_vector_type(N), aligned(sizeof(Elt))));
+    const UN u = *reinterpret_cast<const UN*>(reinterpret_cast<const char*>(p) + FROM * 4);
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[FROM + e] = (float)u[e];
-    }
-    load_elts<Elt, E, FROM + N>(p, v);
+    for (int e = 0; e < N; ++e) w[FROM + e] = u[e];
+    load_words<Elt, E, FROM + N>(p, w);
+  } else if constexpr (LEFT == 2) {
+    w[FROM] = __builtin_bit_cast(uint16_t, p[E - 1]);
   }
 }
+template <typename Elt, int E, bool TAIL>
+__device__ __forceinline__ void load_some(const Elt* p, int n, uint32_t (&w)[q8_words<Elt, E>()]) {
+#pragma unroll
+  for (int i = 0; i < q8_words<Elt, E>(); ++i) w[i] = 0;
+  if (n >= E) {
+    load_words<Elt, E>(p, w);
+  } else if (TAIL && n > 0) {
+#pragma unroll
+    for (int e = 0; e < E - 1; ++e)
+      if (e < n) {
+        if constexpr (sizeof(Elt) == 2) w[e / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[e]) << (e % 2 * 16);
+        else w[e] = __builtin_bit_cast(uint32_t, p[e]);
+      }
+  }
+}
+template <typename Elt>
+__device__ __forceinline__ float word_elt(const uint32_t* w, int e) {
+  if constexpr (sizeof(Elt) == 2) return (float)__builtin_bit_cast(Elt, (uint16_t)(w[e / 2] >> (e % 2 * 16)));
+  else return __builtin_bit_cast(float, w[e]);
+}
+// Floats to the E elements at p.
 template <typename Elt, int E, int FROM = 0>
 __device__ __forceinline__ void store_elts(Elt* p, const float (&v)[E]) {
   constexpr int N = E - FROM >= 8 && sizeof(Elt) == 2 ? 8 : (E - FROM >= 4 ? 4 : (E - FROM >= 2 ? 2 : 1));
@@ -154,68 +202,97 @@ __device__ __forceinline__ void store_elts(Elt* p, const float (&v)[E]) {
   }
 }
 
-// Chunk at channel c0 of a row: its values (zero past C) after the residual's addition, which it
-// stores.  `again`: the second reading of a row that is not held in registers.
-template <typename Elt, int T>
-__device__ __forceinline__ void q8_load(const Q8RowsArgs& a, int64_t row, int c0, bool again, float (&v)[q8_chunk(T, sizeof(Elt)) * T]) {
+// A lane's K chunks of a row (LANES lanes apart), as they lie in memory, and the norm's weight for them.  All loads
+// first: the sum that is stored may be x or the residual, so no later load passes it, and the weight in whole words
+// (16384 rows of 2000 channels, T = 1 fp16, the norm: 42 us; chunk by chunk, the weight channel by channel, 96).
+template <typename Elt, int T, int K>
+struct Q8Chunks {
+  static constexpr int CH = q8_chunk(T, sizeof(Elt)), E = CH * T;
+  uint32_t x[K][q8_words<Elt, E>()], r[K][q8_words<Elt, E>()], g[K][q8_words<Elt, CH>()];
+};
+template <typename Elt, int T, int K>
+__device__ __forceinline__ void q8_weight(const Q8RowsArgs& a, int c, int lanes, Q8Chunks<Elt, T, K>& u) {
+  constexpr int CH = q8_chunk(T, sizeof(Elt));
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int c0 = (c + i * lanes) * CH;
+    if (a.gamma) load_some<Elt, CH, (CH > 1)>(static_cast<const Elt*>(a.gamma) + c0, a.C - c0, u.g[i]);
+  }
+}
+// `again`: the second reading of a row that is not held in registers.
+template <typename Elt, int T, int K>
+__device__ __forceinline__ void q8_load(const Q8RowsArgs& a, int64_t row, bool live, int c, int lanes, bool again, Q8Chunks<Elt, T, K>& u) {
   constexpr int CH = q8_chunk(T, sizeof(Elt)), E = CH * T;
-  const int64_t at = row * ((int64_t)a.C * T) + (int64_t)c0 * T;
+  const int64_t at = row * ((int64_t)a.C * T);
   const bool kept = again && a.sum;
   const Elt* x = static_cast<const Elt*>(kept ? a.sum : a.x) + at;
-  const Elt* r = kept || !a.res ? nullptr : static_cast<const Elt*>(a.res) + at;
-  Elt* out = again || !a.sum ? nullptr : static_cast<Elt*>(a.sum) + at;
-  if (c0 + CH <= a.C) {
-    load_elts<Elt, E>(x, v);
-    if (r) {
-      float u[E];
-      load_elts<Elt, E>(r, u);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = (float)(Elt)(v[e] + u[e]);
-    }
-    if (out) store_elts<Elt, E>(out, v);
-  } else {
+  for (int i = 0; i < K; ++i) {
+    const int c0 = (c + i * lanes) * CH;
+    load_some<Elt, E, (CH > 1)>(x + (int64_t)c0 * T, live ? (a.C - c0) * T : 0, u.x[i]);
+  }
+  if (kept || !a.res) return;
+  const Elt* r = static_cast<const Elt*>(a.res) + at;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+  for (int i = 0; i < K; ++i) {
+    const int c0 = (c + i * lanes) * CH;
+    load_some<Elt, E, (CH > 1)>(r + (int64_t)c0 * T, live ? (a.C - c0) * T : 0, u.r[i]);
+  }
+}
+// Chunk i's values (zero past C) after the residual's addition, which it stores; `sq` collects the sum of their squares.
+template <typename Elt, int T, int K>
+__device__ __forceinline__ void q8_values(const Q8RowsArgs& a, int64_t row, bool live, int c0, bool again, const Q8Chunks<Elt, T, K>& u,
+                                          int i, float (&v)[q8_chunk(T, sizeof(Elt)) * T], float& sq) {
+  constexpr int E = q8_chunk(T, sizeof(Elt)) * T;
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int e = c * T + t;
-        float q = 0.0f;
-        if (c0 + c < a.C) {
-          q = (float)x[e];
-          if (r) q = (float)(Elt)(q + (float)r[e]);
-          if (out) out[e] = (Elt)q;
-        }
-        v[e] = q;
-      }
+  for (int e = 0; e < E; ++e) v[e] = word_elt<Elt>(u.x[i], e);
+  if (a.res && !(again && a.sum)) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (float)(Elt)(v[e] + word_elt<Elt>(u.r[i], e));
+  }
+  if (again) return;
+  if (a.norm) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sq = __builtin_fmaf(v[e], v[e], sq);
+  }
+  if (!a.sum || !live) return;
+  Elt* out = static_cast<Elt*>(a.sum) + row * ((int64_t)a.C * T) + (int64_t)c0 * T;
+  const int n = (a.C - c0) * T;
+  if (n >= E) {
+    store_elts<Elt, E>(out, v);
+  } else if (q8_chunk(T, sizeof(Elt)) > 1 && n > 0) {
+#pragma unroll
+    for (int e = 0; e < E - 1; ++e)
+      if (e < n) out[e] = (Elt)v[e];
   }
 }
 
-// That chunk's planes, times the norm's weight; `top` collects each frequency's largest magnitude,
-// `sq` the sum of squares of the values.
+// That chunk's planes, times the norm's weight.
 template <typename Elt, int T>
-__device__ __forceinline__ void q8_planes(const Q8RowsArgs& a, int c0, const float (&v)[q8_chunk(T, sizeof(Elt)) * T],
-                                          float (&pl)[T][q8_chunk(T, sizeof(Elt))], uint32_t (&top)[n_freqs(T)], float& sq) {
+__device__ __forceinline__ void q8_planes(const Q8RowsArgs& a, const uint32_t* gam, const float (&v)[q8_chunk(T, sizeof(Elt)) * T],
+                                          float (&pl)[T][q8_chunk(T, sizeof(Elt))], Q8Top<n_freqs(T)>& top) {
   constexpr int CH = q8_chunk(T, sizeof(Elt));
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     float g[T], o[T];
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      g[t] = v[c * T + t];
-      sq = __builtin_fmaf(g[t], g[t], sq);
-    }
+    for (int t = 0; t < T; ++t) g[t] = v[c * T + t];
     Dft<T>::run(g, o, a.tw);
-    if (a.gamma) {
-      const float w = (float)static_cast<const Elt*>(a.gamma)[min(c0 + c, a.C - 1)];
 #pragma unroll
-      for (int p = 0; p < T; ++p) o[p] *= w;
-    }
+    for (int p = 0; p < T; ++p) pl[p][c] = o[p];
+  }
+  if (a.gamma) {
 #pragma unroll
-    for (int p = 0; p < T; ++p) {
-      pl[p][c] = o[p];
-      top[freq_of(T, p)] = max(top[freq_of(T, p)], abs_bits(o[p]));
+    for (int c = 0; c < CH; ++c) {
+      const float w = word_elt<Elt>(gam, c);
+#pragma unroll
+      for (int p = 0; p < T; ++p) pl[p][c] *= w;
     }
   }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int p = 0; p < T; ++p) top.take(freq_of(T, p), pl[p][c]);
 }
 
 template <typename Elt, int T>
@@ -250,8 +327,9 @@ __device__ __forceinline__ void q8_store(const Q8RowsArgs& a, int64_t row, int c
 }
 
 // Rows to 8 bits: LPR lanes a row, K chunks a lane.  One read of each operand; the planes stay in
-// registers between the maxima and the codes.  Bound by memory: 65536 rows of 1024 channels, T = 4 fp16, 139 us (5.8 TB/s);
-// the norm with a residual, 50176 rows of 192, 57 us (4.8 TB/s).
+// registers between the maxima and the codes.  Bound by memory, with the vector unit close behind (some 300 operations a
+// wave and 1024 values): 65536 rows of 1024 channels, T = 4 fp16, 143 us (5.6 TB/s), 12608 rows of 384 12.1 (4.8 TB/s);
+// the norm with a residual, 50176 rows of 192, 46 us (5.9 TB/s).
 template <typename Elt, int T, int LPR, int K>
 __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
   constexpr int G = 256 / LPR, CH = q8_chunk(T, sizeof(Elt)), F = n_freqs(T), W = LPR / 64;
@@ -259,32 +337,25 @@ __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
   __shared__ float redSq[2][W > 1 ? W : 1];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
   int turn = 0;
+  Q8Chunks<Elt, T, K> u;
+  q8_weight(a, lane, LPR, u);
   for (int64_t base = (int64_t)blockIdx.x * G; base < a.N; base += (int64_t)gridDim.x * G, turn ^= 1) {
     const int64_t row = base + grp;
     const bool live = row < a.N;
+    q8_load(a, row, live, lane, LPR, false, u);
     float pl[K][T][CH];
-    uint32_t top[F];
+    Q8Top<F> tops;
     float sq = 0.0f;
 #pragma unroll
-    for (int f = 0; f < F; ++f) top[f] = 0;
-    {
-      float v[K][CH * T];
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const int c0 = (lane + i * LPR) * CH;
-        if (live && c0 < a.C) {
-          q8_load<Elt, T>(a, row, c0, false, v[i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < CH * T; ++e) v[i][e] = 0.0f;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < K; ++i) q8_planes<Elt, T>(a, (lane + i * LPR) * CH, v[i], pl[i], top, sq);
+    for (int i = 0; i < K; ++i) {
+      float v[CH * T];
+      q8_values(a, row, live, (lane + i * LPR) * CH, false, u, i, v, sq);
+      q8_planes<Elt, T>(a, u.g[i], v, pl[i], tops);
     }
+    uint32_t top[F];
 #pragma unroll
-    for (int f = 0; f < F; ++f) top[f] = row_max<(LPR < 64 ? LPR : 64)>(top[f]);
-    sq = row_sum<(LPR < 64 ? LPR : 64)>(sq);
+    for (int f = 0; f < F; ++f) top[f] = row_max<(LPR < 64 ? LPR : 64)>(tops.bits(f));
+    if (a.norm) sq = row_sum<(LPR < 64 ? LPR : 64)>(sq);
     if constexpr (W > 1) {
       const int wave = (int)threadIdx.x >> 6;
       if ((threadIdx.x & 63) == 0) {
@@ -309,7 +380,7 @@ __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
     for (int f = 0; f < F; ++f) {
       const float m = q8_top(top[f]);
       inv[f] = q8_inv(m);
-      if (live && lane == 0) a.scales[row * F + f] = m / 127.0f * rstd;
+      if (live && lane == 0) a.scales[row * F + f] = q8_scale(m) * rstd;
     }
     if (live) {
 #pragma unroll
@@ -326,22 +397,24 @@ __global__ void __launch_bounds__(256) eql_q8_rows_wide_kernel(const Q8RowsArgs 
   __shared__ uint32_t redTop[F * 4];
   __shared__ float redSq[4];
   const int64_t row = blockIdx.x;
-  uint32_t top[F];
+  Q8Top<F> tops;
   float sq = 0.0f;
-#pragma unroll
-  for (int f = 0; f < F; ++f) top[f] = 0;
   for (int c0 = (int)threadIdx.x * CH; c0 < a.C; c0 += 256 * CH) {
     float v[CH * T], pl[T][CH];
-    q8_load<Elt, T>(a, row, c0, false, v);
-    q8_planes<Elt, T>(a, c0, v, pl, top, sq);
+    Q8Chunks<Elt, T, 1> u;
+    q8_weight(a, c0 / CH, 0, u);
+    q8_load(a, row, true, c0 / CH, 0, false, u);
+    q8_values(a, row, true, c0, false, u, 0, v, sq);
+    q8_planes<Elt, T>(a, u.g[0], v, pl, tops);
   }
   const int wave = (int)threadIdx.x >> 6;
   sq = row_sum<64>(sq);
 #pragma unroll
-  for (int f = 0; f < F; ++f) top[f] = row_max<64>(top[f]);
+  for (int f = 0; f < F; ++f) {
+    const uint32_t top = row_max<64>(tops.bits(f));
+    if ((threadIdx.x & 63) == 0) redTop[f * 4 + wave] = top;
+  }
   if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-    for (int f = 0; f < F; ++f) redTop[f * 4 + wave] = top[f];
     redSq[wave] = sq;
   }
   __syncthreads();
@@ -352,20 +425,16 @@ __global__ void __launch_bounds__(256) eql_q8_rows_wide_kernel(const Q8RowsArgs 
   for (int f = 0; f < F; ++f) {
     const float m = q8_top(max(max(redTop[f * 4], redTop[f * 4 + 1]), max(redTop[f * 4 + 2], redTop[f * 4 + 3])));
     inv[f] = q8_inv(m);
-    if (threadIdx.x == 0) a.scales[row * F + f] = m / 127.0f * rstd;
+    if (threadIdx.x == 0) a.scales[row * F + f] = q8_scale(m) * rstd;
   }
   for (int c0 = (int)threadIdx.x * CH; c0 < a.pitch; c0 += 256 * CH) {
     float v[CH * T], pl[T][CH], none = 0.0f;
-    uint32_t unused[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) unused[f] = 0;
-    if (c0 < a.C) {
-      q8_load<Elt, T>(a, row, c0, true, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < CH * T; ++e) v[e] = 0.0f;
-    }
-    q8_planes<Elt, T>(a, c0, v, pl, unused, none);
+    Q8Top<F> unused;
+    Q8Chunks<Elt, T, 1> u;
+    q8_weight(a, c0 / CH, 0, u);
+    q8_load(a, row, true, c0 / CH, 0, true, u);
+    q8_values(a, row, true, c0, true, u, 0, v, none);
+    q8_planes<Elt, T>(a, u.g[0], v, pl, unused);
     q8_store<Elt, T>(a, row, c0, pl, inv);
   }
 }
@@ -387,22 +456,20 @@ __global__ void __launch_bounds__(256) eql_q8_pack_kernel(const Q8PackArgs a) {
   if (o >= a.Dpad) return;
   const Elt* w = static_cast<const Elt*>(a.w) + (int64_t)o * a.C * T;
   const int live = o < a.D ? a.C : 0;
-  uint32_t top[F];
-#pragma unroll
-  for (int f = 0; f < F; ++f) top[f] = 0;
+  Q8Top<F> top;
   for (int i = lane; i < live; i += 64) {
     float v[T], pl[T];
     load_group<T, Elt>(w + (int64_t)i * T, v);
     Dft<T>::run(v, pl, a.tw);
 #pragma unroll
-    for (int p = 0; p < T; ++p) top[freq_of(T, p)] = max(top[freq_of(T, p)], abs_bits(pl[p]));
+    for (int p = 0; p < T; ++p) top.take(freq_of(T, p), pl[p]);
   }
   float inv[F];
 #pragma unroll
   for (int f = 0; f < F; ++f) {
-    const float m = q8_top(row_max<64>(top[f]));
+    const float m = q8_top(row_max<64>(top.bits(f)));
     inv[f] = q8_inv(m);
-    if (lane == 0) a.scales[(int64_t)f * a.Dpad + o] = o < a.D ? m / 127.0f * (f < NR ? 1.0f : 2.0f) / (float)T : 0.0f;
+    if (lane == 0) a.scales[(int64_t)f * a.Dpad + o] = o < a.D ? q8_scale(m) * (f < NR ? 1.0f : 2.0f) / (float)T : 0.0f;
   }
   // Four input channels a lane, a word of each plane's codes.
   for (int i = lane * 4; i < a.kblocks * kQ8Block; i += 256) {
