@@ -21,6 +21,7 @@ of gradients raises.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -429,6 +430,14 @@ class EQLayerNorm(torch.nn.Module):
         return "channels=%d, group_order=%d, eps=%g, ckpt8=%s" % (self.channels, self.group_order, self.eps, self.ckpt8)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on_device(t: torch.Tensor):
+    """Where a launch on t's data belongs: its own device, if that is not the current one."""
+    return torch.cuda.device(t.device) if t.is_cuda and t.device.index != torch.cuda.current_device() else _HERE
+
+
 class EQRMSNormFunction(torch.autograd.Function):
     """y = weight s / rms(s) of rows of C'*T features, one weight per channel, shared by its T group
     elements, for s = x + residual (include/eqlinear_rmsnorm.h).  Returns y, or (y, s) with a residual.
@@ -445,7 +454,8 @@ class EQRMSNormFunction(torch.autograd.Function):
         s = torch.empty_like(x2) if residual is not None else None
         train = grad_mode and any(ctx.needs_input_grad[:3])
         rstd = torch.empty(N, dtype=torch.float32, device=x.device) if train else None
-        eqlinear_rmsnorm_fwd(x2, r2, gamma, s, y, rstd, N, Cp, T, eps, x.dtype)
+        with _on_device(x):
+            eqlinear_rmsnorm_fwd(x2, r2, gamma, s, y, rstd, N, Cp, T, eps, x.dtype)
         ctx.set_materialize_grads(False)
         ctx.sizes, ctx.dtype, ctx.shape = (N, Cp, T), x.dtype, x.shape
         if s is None:
@@ -473,7 +483,8 @@ class EQRMSNormFunction(torch.autograd.Function):
         dg = torch.empty(Cp, dtype=ctx.dtype, device=dy2.device) if need_g else None
         n = eqlinear_rmsnorm_bwd_workspace_bytes(N, Cp, T, ctx.dtype)
         ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dy2.device)
-        eqlinear_rmsnorm_bwd(dy2, _rows(s, R), rstd, gamma, ds2, dx, dg, ws, n, N, Cp, T, ctx.dtype)
+        with _on_device(dy2):
+            eqlinear_rmsnorm_bwd(dy2, _rows(s, R), rstd, gamma, ds2, dx, dg, ws, n, N, Cp, T, ctx.dtype)
         dx = dx.reshape(ctx.shape)
         return dx if need_x else None, dx if need_r else None, dg, None, None, None
 
@@ -679,7 +690,8 @@ def eq_quantize_8bit(x: torch.Tensor, group_order: int = 1) -> EQRows8:
     _inference(x)
     N, Cp = _norm_operands(x, None, None, group_order)
     data = torch.empty(max(eqlinear_q8_rows_bytes(N, Cp, group_order), 16), dtype=torch.uint8, device=x.device)
-    eqlinear_q8_quantize(_rows(x, x.shape[-1]), data, N, Cp, group_order, x.dtype)
+    with _on_device(x):
+        eqlinear_q8_quantize(_rows(x, x.shape[-1]), data, N, Cp, group_order, x.dtype)
     return EQRows8(data, x.shape[:-1], Cp, group_order, x.dtype)
 
 
@@ -691,8 +703,9 @@ def eq_rms_norm_8bit(x: torch.Tensor, weight: torch.Tensor | None = None, group_
     R = x.shape[-1]
     data = torch.empty(max(eqlinear_q8_rows_bytes(N, Cp, group_order), 16), dtype=torch.uint8, device=x.device)
     s = torch.empty((N, R), dtype=x.dtype, device=x.device) if residual is not None else None
-    eqlinear_q8_rmsnorm(_rows(x, R), _rows(residual, R) if residual is not None else None,
-                        weight.contiguous() if weight is not None else None, s, data, N, Cp, group_order, eps, x.dtype)
+    with _on_device(x):
+        eqlinear_q8_rmsnorm(_rows(x, R), _rows(residual, R) if residual is not None else None,
+                            weight.contiguous() if weight is not None else None, s, data, N, Cp, group_order, eps, x.dtype)
     rows = EQRows8(data, x.shape[:-1], Cp, group_order, x.dtype)
     return rows if s is None else (rows, s.reshape(x.shape))
 
@@ -723,7 +736,8 @@ class EQLinear8bit(torch.nn.Module):
         if isinstance(layer, EQLinearP4M):
             Dp, Cp, _ = w.shape
             w4 = torch.empty((2 * Dp, 2 * Cp, 4), dtype=w.dtype, device=w.device)
-            eqlinear_p4m_expand_weight(_dense(w), w4, Dp, Cp, w.dtype)
+            with _on_device(w):
+                eqlinear_p4m_expand_weight(_dense(w), w4, Dp, Cp, w.dtype)
             w = w4
         elif not isinstance(layer, EQLinear):
             raise TypeError("expected an EQLinear or an EQLinearP4M, got %s" % type(layer).__name__)
@@ -742,7 +756,8 @@ class EQLinear8bit(torch.nn.Module):
                 (self.out_channels, self.in_channels, self.group_order), tuple(w.shape)))
         if w.device != self.weight8.device:
             raise ValueError("the weight must be on the layer's device (%s), got %s" % (self.weight8.device, w.device))
-        eqlinear_q8_pack_weight(_dense(w), self.weight8, self.out_channels, self.in_channels, self.group_order, w.dtype)
+        with _on_device(w):
+            eqlinear_q8_pack_weight(_dense(w), self.weight8, self.out_channels, self.in_channels, self.group_order, w.dtype)
 
     def forward(self, x, residual: torch.Tensor | None = None) -> torch.Tensor:
         """y = act(x W^T + bias) + residual; x: a tensor [..., C'*T] or EQRows8."""
@@ -764,8 +779,9 @@ class EQLinear8bit(torch.nn.Module):
             raise ValueError("residual must have the output's shape, dtype and device")
         N = math.prod(x.lead_shape)
         y = torch.empty((N, Dp * T), dtype=x.dtype, device=x.data.device)
-        eqlinear_q8_fwd(x.data, self.weight8, self.bias, _rows(residual, Dp * T) if residual is not None else None, y,
-                        N, Cp, Dp, T, x.dtype, _act_code(self.activation))
+        with _on_device(y):
+            eqlinear_q8_fwd(x.data, self.weight8, self.bias, _rows(residual, Dp * T) if residual is not None else None, y,
+                            N, Cp, Dp, T, x.dtype, _act_code(self.activation))
         return y.reshape(shape)
 
     def extra_repr(self) -> str:
