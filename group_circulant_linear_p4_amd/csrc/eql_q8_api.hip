@@ -29,7 +29,9 @@ int check(int64_t N, int64_t Cp, int64_t Dp, int T, int dtype) {
 size_t row_codes(int64_t N, int64_t Cp, int T) { return (size_t)N * (size_t)T * (size_t)q8_pitch(Cp); }
 size_t weight_codes(int64_t Dp, int64_t Cp, int T) { return (size_t)(q8_out(Dp) / 32 * q8_blocks(Cp)) * (size_t)T * 2048; }
 
-// Which kernel a product takes (fp16, rows of input -> output channels).  The small one splits the input channels of each
+// Which kernel a product takes (fp16, rows of input -> output channels).  Up to four rows the token kernel, but for long
+// sums of T = 1, where the small one reads the weight faster (4 rows of 4096 -> 4096: 9.2 us and 5.1, of 4096 -> 1024: 6.1
+// and 5.0; one row the same; T = 4, one row of 4096 -> 1024: 4.9 and 10.2).  The small one splits the input channels of each
 // of its 32 x 32 tiles over eight waves and is the shorter while every tile has a compute unit: T = 4, 256 rows of 1024
 // -> 1024, 256 tiles: 8.5 us and the medium tile's 10.7, of 4096 -> 1024: 24.7 and 33.5; 500 rows, 512 tiles: 14.0 and
 // 11.1.  T = 1, 500 rows of 4096 -> 1024, 512 tiles: 12.1 and 17.7; 1000 rows, 1024 tiles: 21.9 and 18.8.
@@ -39,7 +41,7 @@ size_t weight_codes(int64_t Dp, int64_t Cp, int T) { return (size_t)(q8_out(Dp) 
 // tiles (T = 1, 256 tiles of 1024 -> 1024: 11.6 us and 13.6, of 256 -> 1024: 8.5 and 7.4, 2048 of these: 38.1 and 43.9)
 // and few channels past the last one (T = 2, 65536 rows of 384 -> 384: 53.5 and 44.5).
 Q8Kind product_kind(int64_t N, int64_t Cp, int64_t Dp, int T) {
-  if (N <= kQ8Tokens) return Q8Kind::kToken;
+  if (N <= kQ8Tokens) return T > 1 || N * Cp <= 4096 ? Q8Kind::kToken : Q8Kind::kSmall;
   if (T > kQ8LargeT || ceil_div(N, 32) * ceil_div(Dp, 32) <= (T == 1 ? 512 : 256)) return Q8Kind::kSmall;
   const Q8Tile b = q8_tile(T, true);
   const int64_t tiles = ceil_div(N, 32 * b.mb) * ceil_div(Dp, 128 * b.nb);

@@ -36,7 +36,9 @@ ROWS = [(1, 1, 1), (3, 15, 1), (70, 16, 1), (5, 1000, 1), (9, 4097, 1), (2, 2000
 PRODUCTS = [(1, 1, 1, 1), (1, 64, 32, 1), (5, 65, 33, 1), (33, 200, 100, 1), (1, 1024, 1024, 4), (2, 130, 70, 4), (197, 96, 384, 4),
             (40, 31, 17, 2), (3, 500, 40, 3), (64, 133, 171, 5), (65, 20, 50, 6), (31, 70, 40, 7), (129, 64, 64, 8),
             (7, 33, 66, 9), (40, 129, 20, 10), (17, 65, 35, 11), (66, 30, 31, 12), (5, 40, 33, 13), (33, 66, 9, 14),
-            (9, 17, 65, 15), (35, 64, 32, 16), (1, 4000, 3, 4), (700, 3, 2, 4)]
+            (9, 17, 65, 15), (35, 64, 32, 16), (1, 4000, 3, 4), (700, 3, 2, 4),
+            (20, 1100, 70, 1), (70, 4130, 40, 1), (33, 1024, 64, 1),  # long sums in turns of four steps
+            (1, 4200, 70, 1), (3, 1500, 40, 1)]  # few rows, long sums
 # Enough tiles for the large kernel, ragged in every axis.
 LARGE = [(1500, 70, 1050, 1), (1000, 130, 2100, 2), (1100, 65, 1700, 3), (1030, 100, 1999, 4), (2060, 64, 513, 5),
          (1030, 33, 1100, 6), (530, 130, 2048, 7), (700, 129, 1500, 8), (300, 65, 1700, 9), (300, 40, 1700, 10),
