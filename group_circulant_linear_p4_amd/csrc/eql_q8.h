@@ -115,6 +115,35 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return v;
 }
 
+// Sum of squares of a row from those of its chunks, in one order for every arrangement: chunk j lies on lane j % LPR as
+// its piece j / LPR, and the sums are joined bit by bit of j from the highest down (a missing chunk adds a zero, which
+// changes nothing).  How many lanes take a row depends on N (q8_shape), and with it would the last bit of a sum that each
+// arrangement takes in its own order: 1 / rms, which goes into every scale, differed for one row in six between
+// batches of 4096 and 4097 rows.
+template <int K>
+__device__ __forceinline__ float chunk_sum(float (&q)[K]) {
+#pragma unroll
+  for (int s = K / 2; s > 0; s /= 2)
+#pragma unroll
+    for (int i = 0; i < s; ++i) q[i] += q[i + s];
+  return q[0];
+}
+// The lanes' part, on every lane (LPR 16 or 64).  Where the higher bits are joined already, a rotation within a row of 16
+// lanes is an exchange.
+template <int LPR>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (LPR == 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+    const auto q = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = __builtin_bit_cast(float, (uint32_t)q[0]) + __builtin_bit_cast(float, (uint32_t)q[1]);
+  }
+  v = dpp_add<0x128>(v);  // 8 lanes on
+  v = dpp_add<0x124>(v);
+  v = dpp_add<0x122>(v);
+  return dpp_add<0x121>(v);
+}
+
 struct Q8RowsArgs {
   const void* x;      // [N][C*T]
   const void* res;    // [N][C*T] or null: added to x, the sum rounded to the element type
@@ -333,8 +362,9 @@ __device__ __forceinline__ void q8_store(const Q8RowsArgs& a, int64_t row, int c
 template <typename Elt, int T, int LPR, int K>
 __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
   constexpr int G = 256 / LPR, CH = q8_chunk(T, sizeof(Elt)), F = n_freqs(T), W = LPR / 64;
+  static_assert(LPR == 16 || LPR == 64 || LPR == 256, "lane_sum");
   __shared__ uint32_t redTop[2][W > 1 ? F * W : 1];
-  __shared__ float redSq[2][W > 1 ? W : 1];
+  __shared__ float redSq[2][W > 1 ? 256 : 1];
   const int lane = (int)threadIdx.x % LPR, grp = (int)threadIdx.x / LPR;
   int turn = 0;
   Q8Chunks<Elt, T, K> u;
@@ -345,28 +375,27 @@ __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
     q8_load(a, row, live, lane, LPR, false, u);
     float pl[K][T][CH];
     Q8Top<F> tops;
-    float sq = 0.0f;
+    float sqs[K] = {};
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       float v[CH * T];
-      q8_values(a, row, live, (lane + i * LPR) * CH, false, u, i, v, sq);
+      q8_values(a, row, live, (lane + i * LPR) * CH, false, u, i, v, sqs[i]);
       q8_planes<Elt, T>(a, u.g[i], v, pl[i], tops);
     }
     uint32_t top[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) top[f] = row_max<(LPR < 64 ? LPR : 64)>(tops.bits(f));
-    if (a.norm) sq = row_sum<(LPR < 64 ? LPR : 64)>(sq);
+    float sq = chunk_sum(sqs);
     if constexpr (W > 1) {
       const int wave = (int)threadIdx.x >> 6;
       if ((threadIdx.x & 63) == 0) {
 #pragma unroll
         for (int f = 0; f < F; ++f) redTop[turn][f * W + wave] = top[f];
-        redSq[turn][wave] = sq;
       }
+      redSq[turn][threadIdx.x] = sq;
       __syncthreads();
-      sq = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) sq += redSq[turn][w];
+      const float* q = &redSq[turn][threadIdx.x & 63];
+      sq = (q[0] + q[128]) + (q[64] + q[192]);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         top[f] = 0;
@@ -374,7 +403,7 @@ __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
         for (int w = 0; w < W; ++w) top[f] = max(top[f], redTop[turn][f * W + w]);
       }
     }
-    const float rstd = a.norm ? inv_sqrt(__builtin_fmaf(sq, a.invR, a.eps)) : 1.0f;
+    const float rstd = a.norm ? inv_sqrt(__builtin_fmaf(lane_sum<(LPR < 64 ? LPR : 64)>(sq), a.invR, a.eps)) : 1.0f;
     float inv[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
