@@ -43,17 +43,20 @@ __device__ __forceinline__ u32x4 q8_neg(const u32x4& v) {
 
 #endif
 
-// GELU in its exact form, v Phi(v) = max(v, 0) - |v| (1 - Phi(|v|)), with 1 - Phi(a) = 2^p(a): p is a polynomial of
-// degree 5 with p(0) = -1, fitted to log2(1 - Phi) for the least largest error of the product a (1 - Phi(a)), 5.4e-7
-// (7.2e-7 in fp32 arithmetic over the whole range; p falls without end, so the tail goes to zero).  One transcendental
-// operation and eight others where gelu_erf has two and 13: a product's epilogue is bound by them.  The bound on |v|
-// keeps infinity times zero out; a NaN stays one.
+// GELU, v Phi(v) = max(v, 0) - |v| Q(|v|) with Q = 1 - Phi = 2^p(|v|): p is a polynomial of degree 8 with p(0) = -1,
+// fitted to log2 Q up to 5.6, where |v| Q is off by at most 4.6e-5 of it and 7.9e-8 (in fp32 4.8e-5 and 1.1e-7, and GELU, which
+// is rounded to its own fp32, by 2.4e-7; gelu_erf: 3.8e-7, and 1.7e-3 of the value at -4.2).  Beyond, where it is below 6e-8, p falls
+// without end and faster than log2 Q.  One transcendental operation and eleven others where gelu_erf has two and 13: a
+// product's epilogue is bound by them.  The bound on |v| keeps infinity times zero out; a NaN stays one.
 __device__ __forceinline__ float gelu_power(float v) {
   const float a = __builtin_fabsf(v);
-  float q = __builtin_fmaf(-4.881021735e-4f, a, 7.198718573e-3f);
-  q = __builtin_fmaf(q, a, -5.214663193e-2f);
-  q = __builtin_fmaf(q, a, -0.4595958445f);
-  q = __builtin_fmaf(q, a, -1.151000542f);
+  float q = __builtin_fmaf(-6.174803389e-7f, a, 1.057548525e-5f);
+  q = __builtin_fmaf(q, a, -3.799108526e-5f);
+  q = __builtin_fmaf(q, a, -5.224814522e-4f);
+  q = __builtin_fmaf(q, a, 7.600945886e-3f);
+  q = __builtin_fmaf(q, a, -5.288746953e-2f);
+  q = __builtin_fmaf(q, a, -0.4590758979f);
+  q = __builtin_fmaf(q, a, -1.151120067f);
   q = __builtin_fmaf(q, a, -1.0f);
   return __builtin_fmaf(-__builtin_fminf(a, 1e30f), __builtin_amdgcn_exp2f(q), __builtin_fmaxf(v, 0.0f));
 }

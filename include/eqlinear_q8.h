@@ -64,7 +64,8 @@ size_t eqlinear_q8_weight_bytes(int64_t Dp, int64_t Cp, int T);
 int eqlinear_q8_pack_weight(const void* w, void* w8, int64_t Dp, int64_t Cp, int T, int dtype, void* stream);
 
 /*
- * y[n][d*T+g] = act(layer + bias[d]) + residual, the epilogue in fp32 and rounded once.
+ * y[n][d*T+g] = act(layer + bias[d]) + residual, the epilogue in fp32 and rounded once.  GELU
+ * is v Phi(v) within 2.5e-7, and below zero within 6e-5 of it down to v = -5.6, past which it lies between -6e-8 and 0.
  * rows8, w8: as written by the calls above for these sizes.  bias: [Dp] of `dtype`, or NULL, aligned to
  * the element; act: EQL_ACT_NONE or EQL_ACT_GELU (any other value is EQL_EINVAL); residual: [N][Dp*T], or NULL,
  * may be y.  y: [N][Dp*T] written.  N and Dp that take 2^24 workgroups or more (each at least 32 rows by 32
