@@ -685,6 +685,19 @@ def _inference(*tensors) -> None:
                            "torch.no_grad() or on tensors that need no gradient")
 
 
+class _NoBackward(torch.autograd.Function):
+    """y, computed from parameters that need gradients by something without a backward pass: asking for them raises."""
+
+    @staticmethod
+    def forward(ctx, y, *params):
+        return y.view_as(y)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError("the 8-bit block is an inference form without a backward pass, and its norm has parameters that "
+                           "need a gradient: call it under torch.no_grad(), or freeze them with requires_grad_(False)")
+
+
 def eq_quantize_8bit(x: torch.Tensor, group_order: int = 1) -> EQRows8:
     """x [..., C'*T] as 8-bit rows (a scale for each row and frequency)."""
     _inference(x)
@@ -792,7 +805,7 @@ class EQLinear8bit(torch.nn.Module):
 class EQMLPBlock8bit(torch.nn.Module):
     """Inference form of EQMLPBlock with its two layers in 8-bit integers.  With an RMS norm, the norm writes the
     first layer's 8-bit rows itself; called with a residual (RMS norm only), the block is of x + residual, added in
-    the norm's pass."""
+    the norm's pass.  While the norm's parameters need gradients, a backward pass through the output raises."""
 
     def __init__(self, norm: torch.nn.Module, fc1: EQLinear8bit, fc2: EQLinear8bit):
         super().__init__()
@@ -806,7 +819,9 @@ class EQMLPBlock8bit(torch.nn.Module):
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         _inference(x, residual)
         with torch.no_grad():
-            return self._forward(x, residual)
+            y = self._forward(x, residual)
+        trained = [p for p in self.parameters() if p.requires_grad] if torch.is_grad_enabled() else []
+        return _NoBackward.apply(y, *trained) if trained else y
 
     def _forward(self, x: torch.Tensor, residual) -> torch.Tensor:
         n = self.norm
