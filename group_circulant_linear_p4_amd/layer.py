@@ -22,6 +22,7 @@ of gradients raises.
 from __future__ import annotations
 
 import contextlib
+import functools
 import math
 
 import torch
@@ -38,6 +39,24 @@ from . import (EQL_ACT_GELU, EQL_ACT_NONE, EQL_PACK_BWDX, EQL_PACK_FWD, eqlinear
                eqlinear_packed_weight_bytes, eqlinear_q8_fwd, eqlinear_q8_pack_weight, eqlinear_q8_quantize,
                eqlinear_q8_rmsnorm, eqlinear_q8_rows_bytes, eqlinear_q8_weight_bytes, eqlinear_rmsnorm_bwd,
                eqlinear_rmsnorm_bwd_workspace_bytes, eqlinear_rmsnorm_fwd)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on_device(t: torch.Tensor):
+    """Where a launch on t's data belongs: its own device, if that is not the current one."""
+    return torch.cuda.device(t.device) if t.is_cuda and t.device.index != torch.cuda.current_device() else _HERE
+
+
+def _on_its_device(run):
+    """A forward or backward pass whose launches go to its first tensor's device and that device's current stream."""
+    @functools.wraps(run)
+    def there(ctx, *args):
+        t = next((v for v in args if v is not None), None)
+        with _HERE if t is None else _on_device(t):
+            return run(ctx, *args)
+    return there
 
 
 def _dense(t: torch.Tensor) -> torch.Tensor:
@@ -63,6 +82,7 @@ class EQLinearFunction(torch.autograd.Function):
     """y[..., D'*T] = x[..., C'*T] W^T with W[d*T+g, c*T+h] = w[d, c, (g-h) mod T]."""
 
     @staticmethod
+    @_on_its_device
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, keep_spectra: bool = True):
         Dp, Cp, T = w.shape
         if x.shape[-1] != Cp * T:
@@ -88,6 +108,7 @@ class EQLinearFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @_on_its_device
     def backward(ctx, dy: torch.Tensor):
         x2, w, ws = ctx.saved_tensors
         Dp, Cp, T = w.shape
@@ -139,6 +160,7 @@ class EQLinearFusedFunction(torch.autograd.Function):
     and eqlinear_bwd_w on dpre; the residual's gradient is dy."""
 
     @staticmethod
+    @_on_its_device
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, b, r, act, grad_mode: bool, keep_spectra: bool = True):
         Dp, Cp, T = w.shape
         if x.shape[-1] != Cp * T:
@@ -184,6 +206,7 @@ class EQLinearFusedFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @_on_its_device
     def backward(ctx, dy: torch.Tensor):
         x2, w, pre, wsw = ctx.saved_tensors
         Dp, Cp, T = w.shape
@@ -271,6 +294,7 @@ class EQLinearP4MFunction(torch.autograd.Function):
     the weight gradient is the C_4 one folded back onto the shared parameters."""
 
     @staticmethod
+    @_on_its_device
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, keep_spectra: bool = True):
         Dp, Cp, G = w.shape
         if G != 8:
@@ -300,6 +324,7 @@ class EQLinearP4MFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @_on_its_device
     def backward(ctx, dy: torch.Tensor):
         x2, w4, ws = ctx.saved_tensors
         Dp, Cp = ctx.p4m_shape
@@ -358,6 +383,7 @@ class EQLayerNormFunction(torch.autograd.Function):
     statistics, or with ckpt8 the normalised rows in 8 bits and 1 / std."""
 
     @staticmethod
+    @_on_its_device
     def forward(ctx, x: torch.Tensor, gamma, beta, T: int, eps: float, ckpt8: bool, grad_mode: bool):
         R = x.shape[-1]
         if T < 1 or R % T != 0:
@@ -388,6 +414,7 @@ class EQLayerNormFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @_on_its_device
     def backward(ctx, dy: torch.Tensor):
         x2, ckpt, mean, rstd, gamma = ctx.saved_tensors
         N, Cp, T = ctx.sizes
@@ -430,20 +457,13 @@ class EQLayerNorm(torch.nn.Module):
         return "channels=%d, group_order=%d, eps=%g, ckpt8=%s" % (self.channels, self.group_order, self.eps, self.ckpt8)
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on_device(t: torch.Tensor):
-    """Where a launch on t's data belongs: its own device, if that is not the current one."""
-    return torch.cuda.device(t.device) if t.is_cuda and t.device.index != torch.cuda.current_device() else _HERE
-
-
 class EQRMSNormFunction(torch.autograd.Function):
     """y = weight s / rms(s) of rows of C'*T features, one weight per channel, shared by its T group
     elements, for s = x + residual (include/eqlinear_rmsnorm.h).  Returns y, or (y, s) with a residual.
     Kept for the backward: s and the rows' 1 / rms."""
 
     @staticmethod
+    @_on_its_device
     def forward(ctx, x: torch.Tensor, residual, gamma, T: int, eps: float, grad_mode: bool):
         N, Cp = _norm_operands(x, residual, gamma, T)
         R = Cp * T
@@ -454,8 +474,7 @@ class EQRMSNormFunction(torch.autograd.Function):
         s = torch.empty_like(x2) if residual is not None else None
         train = grad_mode and any(ctx.needs_input_grad[:3])
         rstd = torch.empty(N, dtype=torch.float32, device=x.device) if train else None
-        with _on_device(x):
-            eqlinear_rmsnorm_fwd(x2, r2, gamma, s, y, rstd, N, Cp, T, eps, x.dtype)
+        eqlinear_rmsnorm_fwd(x2, r2, gamma, s, y, rstd, N, Cp, T, eps, x.dtype)
         ctx.set_materialize_grads(False)
         ctx.sizes, ctx.dtype, ctx.shape = (N, Cp, T), x.dtype, x.shape
         if s is None:
@@ -467,6 +486,7 @@ class EQRMSNormFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @_on_its_device
     def backward(ctx, dy, ds=None):
         s, rstd, gamma = ctx.saved_tensors
         N, Cp, T = ctx.sizes
@@ -483,8 +503,7 @@ class EQRMSNormFunction(torch.autograd.Function):
         dg = torch.empty(Cp, dtype=ctx.dtype, device=dy2.device) if need_g else None
         n = eqlinear_rmsnorm_bwd_workspace_bytes(N, Cp, T, ctx.dtype)
         ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dy2.device)
-        with _on_device(dy2):
-            eqlinear_rmsnorm_bwd(dy2, _rows(s, R), rstd, gamma, ds2, dx, dg, ws, n, N, Cp, T, ctx.dtype)
+        eqlinear_rmsnorm_bwd(dy2, _rows(s, R), rstd, gamma, ds2, dx, dg, ws, n, N, Cp, T, ctx.dtype)
         dx = dx.reshape(ctx.shape)
         return dx if need_x else None, dx if need_r else None, dg, None, None, None
 
@@ -539,6 +558,7 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
     branch's gradient dy."""
 
     @staticmethod
+    @_on_its_device
     def forward(ctx, x: torch.Tensor, gamma, beta, w1, b1, w2, b2, eps: float, grad_mode: bool):
         Hp, Cp, T = w1.shape
         if w2.shape != (Cp, Hp, T):
@@ -573,6 +593,7 @@ class EQMLPBlock8bitFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @_on_its_device
     def backward(ctx, dy: torch.Tensor):
         h8, rstd, pre8, gamma, beta, w1, w2 = ctx.saved_tensors
         Hp, Cp, T = w1.shape
