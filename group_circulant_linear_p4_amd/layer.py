@@ -744,10 +744,20 @@ def eq_rms_norm_8bit(x: torch.Tensor, weight: torch.Tensor | None = None, group_
     return rows if s is None else (rows, s.reshape(x.shape))
 
 
+def _convertible(m, classes) -> None:
+    """Refuses a module whose call is more than its class's formula: only that goes into the 8-bit form."""
+    cls = next((c for c in classes if isinstance(m, c)), None)
+    if cls is None:
+        raise TypeError("expected an %s, got %s" % (" or an ".join(c.__name__ for c in classes), type(m).__name__))
+    if not _as_made(m, cls):
+        raise ValueError("the 8-bit form of this %s would leave out its hooks or its own forward" % type(m).__name__)
+
+
 class EQLinear8bit(torch.nn.Module):
     """Inference form of EQLinear in 8-bit integers: the weight's half spectrum with a scale for each output
     channel and frequency, packed once; activations quantised as they come, or given as EQRows8.  Made by
-    from_float, from an EQLinear or an EQLinearP4M (as the layer over C_4 on twice the channels that it runs as).
+    from_float, from an EQLinear or an EQLinearP4M (as the layer over C_4 on twice the channels that it runs as)
+    without hooks or a forward of its own.
     Its outputs are those of the rounded layer, about 1% of their norm off the exact one."""
 
     def __init__(self, in_channels: int, out_channels: int, group_order: int, bias: bool = False,
@@ -766,6 +776,7 @@ class EQLinear8bit(torch.nn.Module):
     @classmethod
     @torch.no_grad()
     def from_float(cls, layer: torch.nn.Module) -> "EQLinear8bit":
+        _convertible(layer, (EQLinear, EQLinearP4M))
         w, bias, act = layer.weight.detach(), getattr(layer, "bias", None), getattr(layer, "activation", None)
         if isinstance(layer, EQLinearP4M):
             Dp, Cp, _ = w.shape
@@ -773,8 +784,6 @@ class EQLinear8bit(torch.nn.Module):
             with _on_device(w):
                 eqlinear_p4m_expand_weight(_dense(w), w4, Dp, Cp, w.dtype)
             w = w4
-        elif not isinstance(layer, EQLinear):
-            raise TypeError("expected an EQLinear or an EQLinearP4M, got %s" % type(layer).__name__)
         Dp, Cp, T = w.shape
         made = cls(Cp, Dp, T, bias is not None, act, device=w.device, dtype=w.dtype)
         made.pack(w)
@@ -824,9 +833,10 @@ class EQLinear8bit(torch.nn.Module):
 
 
 class EQMLPBlock8bit(torch.nn.Module):
-    """Inference form of EQMLPBlock with its two layers in 8-bit integers.  With an RMS norm, the norm writes the
-    first layer's 8-bit rows itself; called with a residual (RMS norm only), the block is of x + residual, added in
-    the norm's pass.  While the norm's parameters need gradients, a backward pass through the output raises."""
+    """Inference form of EQMLPBlock with its two layers in 8-bit integers (of a block whose call, and its layers', is
+    as it is made: no hooks, no forward of its own).  With an RMS norm, the norm writes the first layer's 8-bit rows
+    itself; called with a residual (RMS norm only), the block is of x + residual, added in the norm's pass.  While
+    the norm's parameters need gradients, a backward pass through the output raises."""
 
     def __init__(self, norm: torch.nn.Module, fc1: EQLinear8bit, fc2: EQLinear8bit):
         super().__init__()
@@ -835,6 +845,9 @@ class EQMLPBlock8bit(torch.nn.Module):
     @classmethod
     def from_float(cls, block: EQMLPBlock) -> "EQMLPBlock8bit":
         """The norm is the block's own; the layers are packed anew."""
+        _convertible(block, (EQMLPBlock,))
+        for m in (block.fc1, block.fc2):
+            _convertible(m, (EQLinear, EQLinearP4M))
         return cls(block.norm, EQLinear8bit.from_float(block.fc1), EQLinear8bit.from_float(block.fc2))
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:

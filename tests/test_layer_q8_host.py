@@ -30,3 +30,65 @@ def test_a_block_with_a_trained_norm_refuses_the_backward_pass():
     block.norm.requires_grad_(False)
     y = block(x.detach())
     assert not y.requires_grad
+
+
+@pytest.fixture
+def packed(monkeypatch):
+    """Weights handed to the packing launch."""
+    seen = []
+    monkeypatch.setattr(layer, "eqlinear_q8_pack_weight", lambda w, *a: seen.append(w))
+    monkeypatch.setattr(layer, "eqlinear_p4m_expand_weight", lambda *a: None)
+    return seen
+
+
+class Scaled(layer.EQLinear):
+    def forward(self, x, residual=None):
+        return 3 * super().forward(x, residual)
+
+
+class Renamed(layer.EQLinear):
+    """Computes what EQLinear does."""
+
+
+def test_from_float_takes_what_it_can_keep(packed):
+    for made in (layer.EQLinear(4, 6, 4, bias=True, activation="gelu"), Renamed(4, 6, 4), layer.EQLinearP4M(4, 6)):
+        q = layer.EQLinear8bit.from_float(made)
+        assert isinstance(q, layer.EQLinear8bit) and (q.bias is None) == (getattr(made, "bias", None) is None)
+    assert len(packed) == 3
+    for norm in ("layer", "rms"):
+        block = layer.EQMLPBlock(4, 6, 4, norm=norm)
+        q = layer.EQMLPBlock8bit.from_float(block)
+        assert q.norm is block.norm and q.fc1.activation == "gelu"
+
+
+def test_from_float_refuses_hooks_and_other_forwards(packed):
+    def hooked(register):
+        made = layer.EQLinear(4, 6, 4)
+        getattr(made, register)(lambda *a: None)
+        return made
+    patched, p4m = layer.EQLinear(4, 6, 4), layer.EQLinearP4M(4, 6)
+    patched.forward = lambda x, residual=None: x
+    p4m.register_forward_hook(lambda *a: None)
+    for bad in (Scaled(4, 6, 4), hooked("register_forward_hook"), hooked("register_forward_pre_hook"),
+                hooked("register_full_backward_hook"), patched, p4m):
+        with pytest.raises(ValueError):
+            layer.EQLinear8bit.from_float(bad)
+    block = layer.EQMLPBlock(4, 6, 4)
+    block.fc2.register_forward_hook(lambda *a: None)
+    with pytest.raises(ValueError):
+        layer.EQMLPBlock8bit.from_float(block)
+    block = layer.EQMLPBlock(4, 6, 4)
+    block.register_forward_hook(lambda *a: None)
+    with pytest.raises(ValueError):
+        layer.EQMLPBlock8bit.from_float(block)
+
+    class Other(layer.EQMLPBlock):
+        def forward(self, x):
+            return x - super().forward(x)
+    with pytest.raises(ValueError):
+        layer.EQMLPBlock8bit.from_float(Other(4, 6, 4))
+    with pytest.raises(TypeError):
+        layer.EQMLPBlock8bit.from_float(torch.nn.Sequential())
+    with pytest.raises(TypeError):
+        layer.EQLinear8bit.from_float(torch.nn.Linear(4, 4))
+    assert not packed
