@@ -791,6 +791,22 @@ class EQLinear8bit(torch.nn.Module):
             made.bias.copy_(bias)
         return made
 
+    # The packed weight's size is no sign of its sizes (whole tiles of channels): a state holds them beside it.
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        destination[prefix + "sizes"] = torch.tensor([self.out_channels, self.in_channels, self.group_order])
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs):
+        key, own = prefix + "sizes", [self.out_channels, self.in_channels, self.group_order]
+        sizes = state_dict[key].tolist() if key in state_dict else own
+        if sizes != own:
+            error_msgs.append("%sweight8 is of [output channels, input channels, group order] = %s, the layer of %s" % (
+                prefix, sizes, own))
+            return
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys, unexpected_keys, error_msgs)
+        if key in unexpected_keys:
+            unexpected_keys.remove(key)
+
     @torch.no_grad()
     def pack(self, w: torch.Tensor) -> None:
         """Packs a weight [D', C', T]."""

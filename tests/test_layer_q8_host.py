@@ -92,3 +92,26 @@ def test_from_float_refuses_hooks_and_other_forwards(packed):
     with pytest.raises(TypeError):
         layer.EQLinear8bit.from_float(torch.nn.Linear(4, 4))
     assert not packed
+
+
+def test_a_state_of_other_sizes_is_refused():
+    """A packed weight is bytes: 12 outputs of 8 inputs take as many as 8 of 12, or as 30 of 20."""
+    made = layer.EQLinear8bit(8, 12, 4)
+    made.weight8.random_(0, 255)
+    state = made.state_dict()
+    again = layer.EQLinear8bit(8, 12, 4)
+    again.load_state_dict(state)
+    assert torch.equal(again.weight8, made.weight8)
+    for sizes in ((12, 8, 4), (20, 30, 4)):
+        other = layer.EQLinear8bit(*sizes)
+        assert other.weight8.numel() == made.weight8.numel()
+        for strict in (True, False):
+            with pytest.raises(RuntimeError, match="channels"):
+                other.load_state_dict(state, strict=strict)
+        assert not other.weight8.any()
+    # Within a model, under a prefix; a state saved without the sizes is taken as it was.
+    model = torch.nn.Sequential(layer.EQLinear8bit(8, 12, 4), layer.EQLinear8bit(12, 8, 4))
+    model.load_state_dict(model.state_dict())
+    with pytest.raises(RuntimeError):
+        torch.nn.Sequential(layer.EQLinear8bit(12, 8, 4), layer.EQLinear8bit(8, 12, 4)).load_state_dict(model.state_dict())
+    again.load_state_dict({"weight8": made.weight8})
