@@ -172,6 +172,15 @@ def _current_stream():
     return _raw_stream()
 
 
+def _forget_stream() -> None:
+    global _raw_stream
+    _raw_stream = None
+
+
+# In a forked child torch refuses the GPU, which only the long way asks.
+os.register_at_fork(after_in_child=_forget_stream)
+
+
 def _stream(stream):
     if stream is None:
         return (_raw_stream or _current_stream)() or None
