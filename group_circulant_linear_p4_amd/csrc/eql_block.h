@@ -25,12 +25,6 @@ constexpr NormShape norm_shape(int64_t chunks) {
   return {lpr, k > 6 ? 8 : (k > 4 ? 6 : k)};
 }
 
-// The RMS norm's forward: from 65 to 80 chunks five on each of 16 lanes, where norm_shape's two on each of 64 are half
-// empty (5003 rows of R = 513 fp16, T = 3: 7.5 us and 6.7; backward, with three times the registers, 12.4 and 15.6).
-constexpr NormShape rms_shape(int64_t chunks) {
-  return chunks > 64 && chunks <= 80 ? NormShape{16, 5} : norm_shape(chunks);
-}
-
 hipError_t launch_ckpt_pack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_ckpt_unpack(bool f16, bool stream, const CkptArgs& a, unsigned grid, hipStream_t s);
 hipError_t launch_epi8(bool f16, bool stream, const Epi8Args& a, unsigned grid, hipStream_t s);

@@ -282,7 +282,7 @@ int eqlinear_rmsnorm_fwd(const void* x, const void* residual, const void* gamma,
     if (N > kMaxGrid / 4) return EQL_EINVAL;
     return status_of(launch_rms_fwd_wide(f16, a, s));
   }
-  const NormShape sh = rms_shape(ceil_div(a.R, 8));
+  const NormShape sh = norm_shape(ceil_div(a.R, 8));
   a.table = norm_table(sh.lpr, a.R, T, elt_bytes(dtype), 1);
   const int64_t grid = norm_fwd_grid(ceil_div(N, 256 / sh.lpr));
   const int64_t moved = elt_bytes(dtype) * (2 + (residual ? 1 : 0) + (sum ? 1 : 0));

@@ -8,7 +8,6 @@ template <typename Elt, int LPR, bool WHOLE, bool STREAM>
 static const void* fwd_k(int k) {
   if constexpr (LPR <= 64) {
     if (k == 1) return (const void*)&eql_rms_fwd_kernel<Elt, LPR, 1, WHOLE, STREAM>;
-    if (LPR == 16 && k == 5) return (const void*)&eql_rms_fwd_kernel<Elt, 16, 5, WHOLE, STREAM>;
   } else {
     if (k == 6) return (const void*)&eql_rms_fwd_kernel<Elt, LPR, 6, WHOLE, STREAM>;
     if (k == 8) return (const void*)&eql_rms_fwd_kernel<Elt, LPR, 8, WHOLE, STREAM>;
