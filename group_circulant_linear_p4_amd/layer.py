@@ -711,7 +711,7 @@ class _NoBackward(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, y, *params):
-        return y.view_as(y)
+        return y.detach()  # no view of y to autograd, which would refuse to have it changed in place
 
     @staticmethod
     def backward(ctx, dy):

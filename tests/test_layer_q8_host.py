@@ -11,7 +11,7 @@ class Doubled(torch.nn.Module):
     """In an 8-bit layer's place: 2 x + residual, without parameters."""
 
     def forward(self, x, residual=None):
-        return 2 * x if residual is None else 2 * x + residual
+        return 2 * x if residual is None else (2 * x + residual).reshape(x.shape)
 
 
 def test_a_block_with_a_trained_norm_refuses_the_backward_pass():
@@ -23,6 +23,10 @@ def test_a_block_with_a_trained_norm_refuses_the_backward_pass():
     with pytest.raises(RuntimeError, match="backward"):
         (y * other).sum().backward()
     assert block.norm.weight.grad is None
+    y = block(x)
+    y += 1  # in place, also where fc2 returns a view
+    with pytest.raises(RuntimeError, match="backward"):
+        (y * other).sum().backward()
     with torch.no_grad():
         assert not block(x).requires_grad
     with pytest.raises(RuntimeError):
