@@ -7,7 +7,8 @@
 // group values the transform would leave 8 bits: four codes add up to ten.)  With the planes of
 // eql_device.h, every row n has for each frequency f (f < NR: plane f; then one for each Re / Im pair)
 //     m = max over channels of |plane| (both planes of a pair), at least 2^-100,
-//     code = plane * (127 (1 / m)) rounded to nearest even,  scale[n][f] = m / 127,
+//     code = plane * (127 * (1 / m)) rounded to nearest even,  scale[n][f] = m / 127
+// with the reciprocal and each product rounded to fp32,
 // and the weight the same for each output channel, with the inverse transform's 1 / T (pairs: 2 / T)
 // in its scales.  A row with an infinity or a NaN among a frequency's planes has the scale NaN there.
 //
@@ -357,8 +358,8 @@ __device__ __forceinline__ void q8_store(const Q8RowsArgs& a, int64_t row, int c
 
 // Rows to 8 bits: LPR lanes a row, K chunks a lane.  One read of each operand; the planes stay in
 // registers between the maxima and the codes.  Bound by memory, with the vector unit close behind (some 300 operations a
-// wave and 1024 values): 65536 rows of 1024 channels, T = 4 fp16, 143 us (5.6 TB/s), 12608 rows of 384 12.1 (4.8 TB/s);
-// the norm with a residual, 50176 rows of 192, 46 us (5.9 TB/s).
+// wave and 1024 values): 65536 rows of 1024 channels, T = 4 fp16, 144 us (5.6 TB/s), 12608 rows of 384 13.1 (4.4 TB/s;
+// 11.9 where the rows are in the last-level cache); the norm with a residual, 50176 rows of 192, 50 us (5.4 TB/s).
 template <typename Elt, int T, int LPR, int K>
 __global__ void __launch_bounds__(256) eql_q8_rows_kernel(const Q8RowsArgs a) {
   constexpr int G = 256 / LPR, CH = q8_chunk(T, sizeof(Elt)), F = n_freqs(T), W = LPR / 64;

@@ -31,15 +31,21 @@ size_t weight_codes(int64_t Dp, int64_t Cp, int T) { return (size_t)(q8_out(Dp) 
 
 // Which kernel a product takes (fp16, rows of input -> output channels).  Up to four rows the token kernel, but for long
 // sums of T = 1, where the small one reads the weight faster (4 rows of 4096 -> 4096: 9.2 us and 5.1, of 4096 -> 1024: 6.1
-// and 5.0; one row the same; T = 4, one row of 4096 -> 1024: 4.9 and 10.2).  The small one splits the input channels of each
-// of its 32 x 32 tiles over eight waves and is the shorter while every tile has a compute unit: T = 4, 256 rows of 1024
-// -> 1024, 256 tiles: 8.5 us and the medium tile's 10.7, of 4096 -> 1024: 24.7 and 33.5; 500 rows, 512 tiles: 14.0 and
-// 11.1.  T = 1, 500 rows of 4096 -> 1024, 512 tiles: 12.1 and 17.7; 1000 rows, 1024 tiles: 21.9 and 18.8.
+// and 5.0; one row the same).  For T > 1 it is the shorter one at every T of 2, 3, 4, 5, 8, 12 and 16 with 256 to 4096 -> 1024
+// channels (one row of 4096: 3.6 us and 6.2 at T = 2, 4.5 and 10.3 at T = 4, 16.0 and 120 at T = 16; four rows 5.7 and 6.9, 8.8 and
+// 11.5, 35.7 and 122) and level or shorter with 1024 -> 4096 but for T = 12 (two rows 16.7 and 15.0, four 22.8 and 15.3).
+// The small one splits the input channels of each of its 32 x 32 tiles over eight waves and is the shorter while every
+// tile has a compute unit and the sums are long: T = 4, 256 rows of 1024 -> 1024, 256 tiles: 8.5 us and the medium tile's 10.7, of
+// 4096 -> 1024: 24.7 and 33.5; 500 rows, 512 tiles: 14.0 and 11.1.  T = 1, 500 rows of 4096 -> 1024, 512 tiles: 12.1 and 17.7;
+// 1000 rows, 1024 tiles: 21.9 and 18.8.  (Where it is not, the rule does not follow: T = 4, 64 to 500 rows of 96 -> 384: 5.2 and 4.3;
+// T = 8, 64 to 1000 rows of 256 -> 256: 8.7 to 11.1 and 7.8 to 8.1.)
 // The big tile reads the operands least, once it has a tile for most compute units: T = 4, 12608 rows of 384 -> 96, 197
 // tiles: 10.8 us and the medium one's 11.9; 1000 rows of 1024 -> 1024, 128 tiles: 15.0 and 12.2.  For T <= 2 it is 256
 // channels wide instead of 128 and four workgroups of the medium one share a compute unit, so it needs long sums or many
 // tiles (T = 1, 256 tiles of 1024 -> 1024: 11.6 us and 13.6, of 256 -> 1024: 8.5 and 7.4, 2048 of these: 38.1 and 43.9)
-// and few channels past the last one (T = 2, 65536 rows of 384 -> 384: 53.5 and 44.5).
+// and few channels past the last one (T = 2, 65536 rows of 384 -> 384: 53.5 and 44.5).  Where these rules are
+// furthest off: T = 4, 256 rows of 1024 -> 4096 take 22.9 us on the medium tile and 15.5 on the big one; T = 1, 4096 rows of
+// 1024 -> 1024 fp32 take 8.8 with the narrower medium tile, 8.5 with the wider one.
 Q8Kind product_kind(int64_t N, int64_t Cp, int64_t Dp, int T) {
   if (N <= kQ8Tokens) return T > 1 || N * Cp <= 4096 ? Q8Kind::kToken : Q8Kind::kSmall;
   if (T > kQ8LargeT || ceil_div(N, 32) * ceil_div(Dp, 32) <= (T == 1 ? 512 : 256)) return Q8Kind::kSmall;

@@ -111,8 +111,8 @@ __device__ __forceinline__ void q8_finish(const Q8FwdArgs& a, const int32_t (&su
 // bytes of every 512 in the weight's operand order), so that the weight spreads over the chip (1024 channels: 128
 // workgroups); lane l takes channel l % 8 and the 16 input channels number l / 8 of each pair of K blocks, its wave
 // every fourth pair.  Dot products of four codes, eight lanes' and four waves' sums added at the end.  Bound by one
-// memory latency after the other (one row, 1024 -> 1024 channels, T = 4 fp16: 3.6 us, 4.2 MB of weight; on the small
-// kernel's tiles 5.8).
+// memory latency after the other (one row, 1024 -> 1024 channels, T = 4 fp16: 3.8 us, 4.2 MB of weight; with the weight in
+// cache 2.8, on the small kernel's tiles then 5.1).
 constexpr int kQ8Tokens = 4;
 template <int T, typename Elt>
 __global__ void __launch_bounds__(256) eql_q8_token_kernel(const Q8FwdArgs a) {
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) eql_q8_token_kernel(const Q8FwdArgs a) {
   const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
   const int ol = lane & 7, piece = lane >> 3;  // piece: K block of the pair, its half, quarter
   const int col0 = (int)blockIdx.x * 8;
-  // The last eight threads' epilogue operands are on their way before the sums.
+  // Eight threads a row end with its outputs (the first 32 at most); their operands are on their way before the sums.
   const int n = (int)threadIdx.x >> 3, col = col0 + ((int)threadIdx.x & 7);
   const bool ends = n < a.f.N && n < kQ8Tokens && col < a.f.Dout;
   float scale[F], res[T], bias = 0.0f;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(256) eql_q8_token_kernel(const Q8FwdArgs a) {
 // Few rows or few output channels: a workgroup takes a 32 x 32 tile of outputs, its waves every so-manieth step
 // of 32 input channels each (operands straight from memory), and adds its integer sums in LDS.  Epilogue: a thread a
 // (row, channel), a row's channels on neighbouring lanes; its operands are on their way before the sums.  Bound by
-// latency (197 rows, 96 -> 384 channels, T = 4 fp16, GELU: 6.4 us; the bytes would take 0.2).
+// latency (197 rows, 96 -> 384 channels, T = 4 fp16, GELU: 6.8 us; the bytes would take 0.2).
 template <int T, typename Elt>
 __global__ void __launch_bounds__(T <= 8 ? 512 : 256) eql_q8_small_kernel(const Q8FwdArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(T <= 8 ? 512 : 256) eql_q8_small_kernel(const 
   const uint32_t xOff = (uint32_t)(lane & 31) * rowBytes + (uint32_t)(lane >> 5) * 16u;
   const int steps = (a.pitch + 31) / 32;
   // Long sums of T = 1 go in turns of four steps next to each other, the next turn's under way: a row's 128 bytes are read
-  // at once (8 rows of 11000 -> 4096 channels, fp16: 9.4 us, with one step a turn 17.1; T = 2 gains nothing, and T = 4 has
+  // at once (8 rows of 11000 -> 4096 channels, fp16: 9.8 us, with one step a turn 17.1; T = 2 gains nothing, and T = 4 has
   // no registers for it).
   constexpr int DEPTH = T == 1 ? 4 : 1;
   u32x4 xa[DEPTH][T], wb[DEPTH][T];
@@ -338,10 +338,11 @@ __global__ void __launch_bounds__(T <= 8 ? 512 : 256) eql_q8_small_kernel(const 
 //     group from the next slot, so the wait for its loads and the barrier come before that group's products.
 //   * The last block is code of its own, which loads nothing ahead but the first residuals, into the registers that the
 //     next operands would have taken (50176 rows of 192 -> 192, T = 4 fp16, with a residual: 42.1 -> 40.6 us).
-// At 65536 rows of 1024 -> 1024, T = 4 fp16: 615 us with a residual, 479 without (825 G integer operations, 1.34 and 0.81
-// GB).  The matrix unit is busy 48% of a long main loop (1.9 P operations/s; these instructions alone, on such codes,
-// reach 3.6, held by the card's power: on zeros the kernel takes 514 and 385 us), and the residual's reads, 4.1 TB/s, come
-// on top of it: both workgroups of a compute unit share the way from L2 that the weight's operands take.
+// At 65536 rows of 1024 -> 1024, T = 4 fp16, call after call: 578 us with a residual, 495 without (825 G integer operations,
+// 1.34 and 0.81 GB), 605 with rows and residual out of the caches.  The matrix unit is busy 36% of that (counted); these instructions
+// alone, on such codes, reach 3.6 P operations/s, held by the card's power: on zeros the kernel takes 517 and 399 us.  The
+// residual's reads, 83 and 118 us of these, hardly overlap the main loops: both workgroups of a compute unit share the way from
+// L2 that the weight's operands take.
 template <int T, typename Elt, int MB, int NB>
 __global__ void __launch_bounds__(256, (T * MB * NB <= 8 ? 2 : 1)) eql_q8_large_kernel(const Q8FwdArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -65,7 +65,8 @@ def values(pl, T):
 
 
 def encode(pl, T):
-    """Codes [T, rows, C] and scales [rows, F] of planes, the codes' two operations in fp32."""
+    """Codes [T, rows, C] and scales [rows, F] of planes, the codes' operations (1 / m, 127 times it, the plane times
+    that), each in fp32."""
     _, groups = frequencies(T)
     codes, scales = np.zeros(pl.shape, np.int8), np.zeros((pl.shape[1], len(groups)))
     for f, where in enumerate(groups):
